@@ -221,7 +221,7 @@ def _own_route(s):
     r = dpg.dpg_route(s["logits"], s["top_k"], renormalize=s["renormalize"])
     out = {"experts": r.experts, "weights": r.weights, "offsets": r.offsets, "rows": r.rows,
            "positions": r.positions,
-           "xs": dpg.dpg_dispatch(s["x"], r.rows, r.offsets, s["top_k"]),
+           "xs": dpg.dpg_dispatch(s["x"], r.positions, r.offsets),
            "y": dpg.dpg_combine(s["ys"], r.positions, r.offsets, r.weights)}
     if s["grad"]:
         out["dys"], out["dweights"] = dpg.dpg_combine_dgrad(s["dy"], s["ys"], r.positions, r.offsets, r.weights)
