@@ -573,3 +573,8 @@ def dpg_wgrad_batched(dy, x, out=None, out_dtype=torch.bfloat16, weight_layout="
     if st:
         raise DpgError(st, "dpg_wgrad_batched")
     return out
+
+
+# ----------------------------------------------------------- expert layers --
+from .experts import (ADAMW_BLOCK, Route, dpg_adamw, dpg_combine, dpg_combine_dgrad, dpg_dispatch,  # noqa: E402,F401
+                      dpg_grouped_dgrad, dpg_grouped_forward, dpg_grouped_wgrad, dpg_route, dpg_route_dgrad)

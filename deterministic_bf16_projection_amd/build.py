@@ -13,7 +13,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdpg.so")
-SOURCES = [os.path.join(HERE, "csrc", "dpg_api.hip"), os.path.join(HERE, "csrc", "planner.cpp")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("dpg_api.hip", "dpg_grouped.hip", "dpg_route.hip", "dpg_adamw.hip",
+                                                   "planner.cpp")]
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 ARCH = "gfx950"
 

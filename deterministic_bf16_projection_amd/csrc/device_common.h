@@ -94,4 +94,38 @@ __device__ __forceinline__ int xcd_remap(int bid, int total) {
   return tall * per + (xcd - tall) * (per - 1) + local;
 }
 
+// ------------------------------------------------------ wave reductions --
+// Six steps of the data-parallel primitives (within rows of 16 lanes, then
+// across rows); lane 63 holds the result.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_f32(float old, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old),
+                                                               __builtin_bit_cast(int, v), CTRL, ROW_MASK, 0xf,
+                                                               false));
+}
+
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp_f32<0x111, 0xf>(v, v));  // row_shr:1
+  v = fmaxf(v, dpp_f32<0x112, 0xf>(v, v));
+  v = fmaxf(v, dpp_f32<0x114, 0xf>(v, v));
+  v = fmaxf(v, dpp_f32<0x118, 0xf>(v, v));
+  v = fmaxf(v, dpp_f32<0x142, 0xa>(v, v));  // row_bcast:15
+  v = fmaxf(v, dpp_f32<0x143, 0xc>(v, v));  // row_bcast:31
+  return lane_f32(v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0x111, 0xf>(0.f, v);
+  v += dpp_f32<0x112, 0xf>(0.f, v);
+  v += dpp_f32<0x114, 0xf>(0.f, v);
+  v += dpp_f32<0x118, 0xf>(0.f, v);
+  v += dpp_f32<0x142, 0xa>(0.f, v);
+  v += dpp_f32<0x143, 0xc>(0.f, v);
+  return lane_f32(v, 63);
+}
+
 }  // namespace dpg

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "api_common.h"
 #include "dpg.h"
 #include "gemm_fast.h"
 #include "gemm_kernel.h"
@@ -184,20 +185,6 @@ std::list<CacheEntry>* g_lru = nullptr;  // most recently used first
 std::unordered_map<PlanKey, std::list<CacheEntry>::iterator, KeyHash>* g_index = nullptr;
 int64_t g_generation = 0;
 
-// CU count of the current device (fast mode only), cached per device id.
-int device_cus() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return kDetCus;
-  if (cached[dev] == 0) {
-    int cus = 0;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-      cus = kDetCus;
-    cached[dev] = cus;
-  }
-  return cached[dev];
-}
-
 bool get_plan(const PlanKey& key_in, Plan* plan) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_lru) {
@@ -234,24 +221,6 @@ PlanKey make_key(int pass, int64_t T, int64_t N, int64_t K, int out, int det, in
   k.cus = det ? kDetCus : (query_device ? device_cus() : kDetCus);
   k.router_arith = pass >= 3 ? g_router_arith.load() : ROUTER_AUTO;
   return k;
-}
-
-// ----------------------------------------------------------- validation --
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Mat {
-  const void* ptr;
-  int64_t ld, rows, cols;
-  int elt;  // bytes per element
-};
-
-dpg_status check_mat(const Mat& m) {
-  if (m.rows < 0 || m.cols < 0) return DPG_ERR_INVALID_ARG;
-  if (m.rows == 0 || m.cols == 0) return DPG_OK;  // empty: pointer and ld unused
-  if (!m.ptr) return DPG_ERR_INVALID_ARG;
-  if (m.ld < m.cols) return DPG_ERR_INVALID_ARG;
-  if (!aligned16(m.ptr) || (m.ld * m.elt) % 16 != 0 || m.cols % 8 != 0) return DPG_ERR_ALIGNMENT;
-  return DPG_OK;
 }
 
 // fixed-order sum of the split partials in the workspace, converted to the output type

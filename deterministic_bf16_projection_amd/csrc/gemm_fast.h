@@ -127,6 +127,15 @@ struct FastOperand {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) g[i] = buf_load16(r, v + (uint32_t)i * vstep);
   }
+  // K-major, the last K tile with `left` (< 64, a multiple of 8) reduction
+  // elements: the chunks past them get an offset beyond any descriptor (a tile
+  // spans less than 2^31 bytes) and read as zero
+  __device__ __forceinline__ void load_tail(rsrc_t r, int tid, int left) {
+    static_assert(KMAJ, "MN-major tiles end with their descriptor");
+    const uint32_t v = voff0 | ((tid & 7) * 8 >= left ? 0x80000000u : 0u);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) g[i] = buf_load16(r, v + (uint32_t)i * vstep);
+  }
 
   __device__ __forceinline__ void store(__bf16* plane, __bf16* /*lo plane: BF16x3 only*/ = nullptr) const {
     if (BLOCK_THREADS < NT && !owner) return;
@@ -268,6 +277,17 @@ struct DmaOperand {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(plane + g * 512), 16, (int)voff[j], 0, 0, 0);
     }
   }
+  // the last K tile with `left` (< 64, a multiple of 8) reduction elements: as
+  // FastOperand::load_tail (row 8 g + l / 8 holds chunk (l ^ l / 8 ^ g) % 8)
+  __device__ __forceinline__ void load_tail(rsrc_t rs, __bf16* plane, int lane, int left) const {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int g = j * NW + group0;
+      const int c = (lane ^ (lane >> 3) ^ g) & 7;
+      const uint32_t v = voff[j] | (c * 8 >= left ? 0x80000000u : 0u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(plane + g * 512), 16, (int)v, 0, 0, 0);
+    }
+  }
 };
 
 // Buffer descriptor of the K tile starting at k0 (32-bit arithmetic only: the
@@ -355,7 +375,9 @@ struct StepCursor {
   int nkt, kt0;     // the unit's K tiles and first K tile
   int row0, col0;   // the unit's tile origin
   int split;
-  int b;            // the unit's problem
+  int b;            // the unit's problem (grouped products: its group)
+  // grouped products only: the group's first row (token) and its row count
+  int base, count;
 };
 
 template <int BM, int BN>
@@ -459,12 +481,14 @@ __device__ __forceinline__ StepCursor sk_next(const UnitMap& m, const StreamKWor
   return sk_cursor<BM, BN>(m, w, c.u + c.nkt);
 }
 
+#include "grouped_units.h"
+
 // Which operands a wave stages: both (four-wave tiles), or only A / only B
 // (eight-wave tiles: waves 0-3 stage A, waves 4-7 stage B).
 enum StageRole { ROLE_BOTH = 0, ROLE_A = 1, ROLE_B = 2 };
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool A_KMAJ, bool B_KMAJ, int OUT, int ROLE, bool X3 = false,
-          bool SK = false>
+          bool SK = false, bool GR = false>
 struct FastGemm {
   static constexpr int BK = 64;
   static constexpr int NT = 64 * WAVES_M * WAVES_N;
@@ -494,6 +518,11 @@ struct FastGemm {
   static constexpr int PLANE_A = BM * BK, PLANE_B = BN * BK, STAGE = (PLANE_A + PLANE_B) * PLANES;
   static constexpr int B_BASE = PLANE_A * PLANES;  // first B plane in a stage
   typedef typename std::conditional<X3, float, __bf16>::type InT;
+  typedef typename std::conditional<GR, GroupedParams, GemmParams>::type Params;
+  // grouped products: forward and input gradient split the output rows into
+  // groups (GR_ROWS), the weight gradient the reduction (one output per group)
+  static constexpr bool GR_ROWS = GR && A_KMAJ;
+  static_assert(!GR || (!X3 && !SK), "grouped products: BF16, whole reductions");
   typedef typename std::conditional<X3, FastOperandX3<BM, A_KMAJ, NTL>, FastOperand<BM, A_KMAJ, NTL>>::type OpA;
   typedef typename std::conditional<X3, FastOperandX3<BN, B_KMAJ, NTL>, FastOperand<BN, B_KMAJ, NTL>>::type OpB;
   // Who stages what.  A K-major A (X in the forward pass, dY in the input
@@ -546,9 +575,14 @@ struct FastGemm {
   // row's 128 contiguous bytes.  Every store instruction then writes 8 whole
   // 128-byte row segments instead of 32 pieces of 32 B: for the FP32
   // input gradient of 4096 -> 1024 at 16384 tokens, 189 -> 139 us.
-  static __device__ __forceinline__ void epilogue(const GemmParams& p, const StepCursor& c, int lane, int wm, int wn,
+  static __device__ __forceinline__ void epilogue(const Params& p, const StepCursor& c, int lane, int wm, int wn,
                                                   f32x16 (&acc)[FM][FN], char* scr) {
     char* out;
+    if constexpr (GR_ROWS) {
+      out = (char*)p.c + (int64_t)c.base * p.ldc * (OUT == OUT_BF16 ? 2 : 4);
+      store_tile<OUT>(out, p.ldc, 0, 0, c.count, p.N, c.row0, c.col0, lane, wm, wn, acc, scr);
+      return;
+    }
     if (OUT == OUT_PARTIAL)
       out = (char*)p.c + ((int64_t)c.b * p.batch_c + (int64_t)c.split * p.split_stride) * 4;
     else
@@ -621,7 +655,7 @@ struct FastGemm {
     }
   }
 
-  static __device__ __forceinline__ void run(__bf16* smem, const GemmParams& p, int ltid, int lane, int wm, int wn) {
+  static __device__ __forceinline__ void run(__bf16* smem, const Params& p, int ltid, int lane, int wm, int wn) {
     // this wave's epilogue buffer, after the two pipeline stages
     char* scr = (char*)(smem + 2 * STAGE) + (wm * WAVES_N + wn) * 4096;
     const InT* A = (const InT*)p.a;
@@ -644,18 +678,37 @@ struct FastGemm {
                         SK ? skw.dp_count * skw.KT + (skw.i1 - skw.i0) : p.tiles_m * p.tiles_n * p.splits * p.batch,
                         p.tiles_m * p.tiles_n * p.splits, split_parts(p.splits, p.kt_total)};
     const int stride = gridDim.x;
-    // the workgroup's unit stream: (tile, K split) units, or its stream-K work
+    GroupMap gm = {};
+    if constexpr (GR) gm = group_map<BM, GR_ROWS>(p, lane);
+    // the workgroup's unit stream: (tile, K split) units, its stream-K work, or
+    // (group, tile) units
     auto first_step = [&]() -> StepCursor {
       if constexpr (SK)
         return sk_cursor<BM, BN>(um, skw, 0);
+      else if constexpr (GR)
+        return group_cursor<BM, BN, GR_ROWS>(p, gm, blockIdx.x);
       else
         return cursor_at<BM, BN>(um, blockIdx.x);
     };
     auto next_step = [&](const StepCursor& c) -> StepCursor {
-      if constexpr (SK)
+      if constexpr (SK) {
         return sk_next<BM, BN>(um, skw, c);
-      else
+      } else if constexpr (GR) {
+        if (c.kt + 1 < c.nkt) {
+          StepCursor n = c;
+          n.kt = c.kt + 1;
+          return n;
+        }
+        return group_cursor<BM, BN, GR_ROWS>(p, gm, c.u + stride);
+      } else {
         return cursor_next<BM, BN>(um, c, stride);
+      }
+    };
+    auto valid = [&](const StepCursor& c) -> bool {
+      if constexpr (GR)
+        return c.u < gm.total;
+      else
+        return cursor_valid(um, c);
     };
     OpA opa;
     OpB opb;
@@ -732,6 +785,25 @@ struct FastGemm {
   } while (0)
     // loads of the step at cursor L (out-of-range steps read nothing)
     auto load = [&](const StepCursor& L) {
+      if constexpr (GR) {
+        const GroupStep g = group_step<GR_ROWS>(p, L, valid(L));
+        if (DO_A) {
+          const rsrc_t r = tile_rsrc<A_KMAJ, BM>(A + g.a, lda, L.row0, g.rows, g.kk, g.K);
+          if constexpr (A_KMAJ) {
+            if (g.kk + BK > g.K)
+              opa.load_tail(r, ltid, g.K - g.kk);
+            else
+              opa.load(r);
+          } else {
+            opa.load(r);
+          }
+        }
+        if (DO_B) {
+          static_assert(!DO_B || !B_KMAJ, "a K-major B is fetched into LDS");
+          opb.load(tile_rsrc<B_KMAJ, BN>(B + g.b, ldb, L.col0, p.N, g.kk, g.K));
+        }
+        return;
+      }
       // a step past the last unit gets empty descriptors (one row, no K left)
       const bool ok = cursor_valid(um, L);
       const int kk = ok ? (L.kt0 + L.kt) * BK : p.K;
@@ -745,6 +817,19 @@ struct FastGemm {
       if (DO_B) opb.store(stage + B_BASE, stage + B_BASE + PLANE_B);
     };
     auto dma = [&](const StepCursor& L, __bf16* stage) {
+      if constexpr (GR) {
+        const GroupStep g = group_step<GR_ROWS>(p, L, valid(L));
+        const rsrc_t ra = tile_rsrc<true, BM>(A + g.a, lda, L.row0, g.rows, g.kk, g.K);
+        const rsrc_t rb = tile_rsrc<true, BN>(B + g.b, ldb, L.col0, p.N, g.kk, g.K);
+        if (g.kk + BK > g.K) {
+          opd.load_tail(ra, stage, lane, g.K - g.kk);
+          if constexpr (B_INTO_LDS) opdb.load_tail(rb, stage + B_BASE, lane, g.K - g.kk);
+        } else {
+          opd.load(ra, stage);
+          if constexpr (B_INTO_LDS) opdb.load(rb, stage + B_BASE);
+        }
+        return;
+      }
       const bool ok = cursor_valid(um, L);
       const int kk = ok ? (L.kt0 + L.kt) * BK : p.K;
       opd.load(tile_rsrc<true, BM>(A + L.b * p.batch_a, lda, L.row0, ok ? p.M : L.row0 + 1, kk, p.K), stage);
@@ -754,7 +839,7 @@ struct FastGemm {
     };
 
     StepCursor C = first_step();
-    if (!cursor_valid(um, C)) return;
+    if (!valid(C)) return;
     StepCursor L = C;
     // prologue: K tile 0 into stage 0, the loads of K tile 1 in flight
     if constexpr (DMA) dma(L, smem);
@@ -788,7 +873,7 @@ struct FastGemm {
     constexpr int NR = (FM + FN) * PLANES;        // fragment reads per k-step
     constexpr int NW = (DO_A ? OpA::NWRITES : 0) + (DO_B ? OpB::NWRITES : 0);  // LDS writes per tile
     constexpr int NV = (DO_A ? OpA::NLOADS : 0) + (DO_B ? OpB::NLOADS : 0);    // buffer loads per tile
-    for (int it = 0; cursor_valid(um, C); ++it) {
+    for (int it = 0; valid(C); ++it) {
       const __bf16* cur = smem + (it & 1) * STAGE;
       __bf16* nxt = smem + ((it + 1) & 1) * STAGE;
       if constexpr (SB) {
@@ -909,8 +994,9 @@ struct FastGemm {
 };
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool A_KMAJ, bool B_KMAJ, int OUT, bool X3 = false,
-          bool SK = false>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) gemm_fast_kernel(GemmParams p) {
+          bool SK = false, bool GR = false>
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1)
+    gemm_fast_kernel(typename std::conditional<GR, GroupedParams, GemmParams>::type p) {
   constexpr int BK = 64;
   constexpr int NT = 64 * WAVES_M * WAVES_N;
   static_assert(NT == 256 || NT == 512, "four or eight waves");
@@ -924,11 +1010,11 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) gemm_fast_kernel(Ge
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   if constexpr (NT == 512) {
     if (wave < 4)
-      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_A, false, SK>::run(smem, p, tid, lane, wm, wn);
+      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_A, false, SK, GR>::run(smem, p, tid, lane, wm, wn);
     else
-      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_B, false, SK>::run(smem, p, tid - 256, lane, wm, wn);
+      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_B, false, SK, GR>::run(smem, p, tid - 256, lane, wm, wn);
   } else {
-    FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_BOTH, X3, SK>::run(smem, p, tid, lane, wm, wn);
+    FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_BOTH, X3, SK, GR>::run(smem, p, tid, lane, wm, wn);
   }
 }
 

@@ -1,0 +1,159 @@
+// Work units of the grouped products: rows sorted by group (expert), group g
+// holding the rows [offsets[g], offsets[g + 1]) of the token-side matrices and
+// its own weight (or weight-gradient) matrix.
+//
+//   forward         Y[r,:]  = X[r,:] . W[g]^T       r in group g
+//   input gradient  dX[r,:] = dY[r,:] . W[g]
+//   weight gradient dW[g]   = sum over r in group g of dY[r,:]^T X[r,:]
+//
+// The group sizes are known on the device only, so the host launches a
+// persistent grid for the largest possible number of units, and every wave
+// finds its units by itself: lane l of a wave sums the tile rows of the groups
+// [l c, (l + 1) c), c = ceil(groups / 64), and a prefix sum over the lanes,
+// held in one register, answers "which lane holds unit u" with one ballot; the
+// group among that lane's c is found with scalar loads.  No table in memory
+// and no launch before the product.  The rows past the last group form one
+// more group without a reduction, whose output rows are written as zeros.
+//
+// The offsets come from device memory unseen by the host: every use clamps
+// them to [0, rows] and a group's end to its start or later, so wrong ones
+// give wrong results but no access outside the matrices.
+//
+// Included by gemm_fast.h inside namespace dpg.
+#pragma once
+
+struct GroupedParams : GemmParams {
+  const int* offsets;  // groups + 1, on the device; offsets[0] is taken as 0
+  int groups;
+  int rows;            // rows of the token-side matrices
+};
+
+typedef __attribute__((address_space(4))) const int const_int_t;
+
+// rows [first, end) of a group, clamped
+__device__ __forceinline__ void group_rows(const int* offsets, int rows, int g, int& first, int& end) {
+  const const_int_t* o = (const const_int_t*)(uintptr_t)offsets;
+  first = g == 0 ? 0 : min(max(o[g], 0), rows);
+  end = min(max(o[g + 1], first), rows);
+}
+
+struct GroupMap {
+  int per_lane;   // groups of one lane
+  int lane_end;   // units of this lane's groups and all before (one value per lane)
+  int grouped;    // units of all groups
+  int total;      // with those of the rows past the last group
+  int tail0;      // first row past the last group
+};
+
+template <int BM, bool ROWS>
+__device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) {
+  GroupMap m = {};
+  if constexpr (!ROWS) {
+    m.total = m.grouped = p.groups * p.tiles_m * p.tiles_n;
+    return m;
+  }
+  m.per_lane = (p.groups + 63) >> 6;
+  int units = 0;
+  int at = 0;
+  const int g0 = lane * m.per_lane;
+  if (g0 < p.groups) at = g0 == 0 ? 0 : min(max(p.offsets[g0], 0), p.rows);
+  for (int i = 0; i < m.per_lane; ++i) {
+    if (g0 + i >= p.groups) break;
+    const int next = min(max(p.offsets[g0 + i + 1], 0), p.rows);
+    units += (max(next, at) - at + BM - 1) / BM;
+    at = next;
+  }
+  units *= p.tiles_n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(units, d);
+    if (lane >= d) units += v;
+  }
+  m.lane_end = units;
+  m.grouped = __builtin_amdgcn_readlane(units, 63);
+  const const_int_t* o = (const const_int_t*)(uintptr_t)p.offsets;
+  m.tail0 = p.groups == 0 ? 0 : min(max(o[p.groups], 0), p.rows);
+  m.total = m.grouped + (p.rows - m.tail0 + BM - 1) / BM * p.tiles_n;
+  return m;
+}
+
+// Unit u of the stream: the units of one group are consecutive, rastered in
+// bands of group_m tile rows, and the XCD remap gives each XCD consecutive
+// units, so that a group's weight is read into one XCD's L2.
+template <int BM, int BN, bool ROWS>
+__device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const GroupMap& m, int unit) {
+  StepCursor c;
+  c.u = unit;
+  c.kt = c.kt0 = c.split = 0;
+  const int id = __builtin_amdgcn_readfirstlane(xcd_remap(min(unit, m.total - 1), m.total));
+  int t, tiles_m;
+  if constexpr (ROWS) {
+    const int l = __builtin_popcountll(__ballot(m.lane_end <= id));
+    if (l < 64) {
+      t = id - (l > 0 ? __builtin_amdgcn_readlane(m.lane_end, l - 1) : 0);
+      c.b = l * m.per_lane;
+      for (int i = 0;; ++i) {
+        int end;
+        group_rows(p.offsets, p.rows, c.b, c.base, end);
+        c.count = end - c.base;
+        tiles_m = (c.count + BM - 1) / BM;
+        if (t < tiles_m * p.tiles_n || i + 1 >= m.per_lane || c.b + 1 >= p.groups) break;
+        t -= tiles_m * p.tiles_n;
+        ++c.b;
+      }
+      c.nkt = p.kt_total;
+    } else {
+      t = id - m.grouped;
+      c.b = p.groups;
+      c.base = m.tail0;
+      c.count = p.rows - m.tail0;
+      tiles_m = (c.count + BM - 1) / BM;
+      c.nkt = 1;
+    }
+  } else {
+    c.b = id / (p.tiles_m * p.tiles_n);
+    t = id - c.b * (p.tiles_m * p.tiles_n);
+    int end;
+    group_rows(p.offsets, p.rows, c.b, c.base, end);
+    c.count = end - c.base;
+    tiles_m = p.tiles_m;
+    c.nkt = max(1, (c.count + 63) >> 6);
+  }
+  const int per_band = p.group_m * p.tiles_n;
+  const int band = t / per_band;
+  const int first_m = band * p.group_m;
+  const int band_rows = max(min(tiles_m - first_m, p.group_m), 1);
+  const int r = t - band * per_band;
+  c.row0 = (first_m + r % band_rows) * BM;
+  c.col0 = (r / band_rows) * BN;
+  return c;
+}
+
+// Where a step's operands lie: element offsets of the group's parts of A and
+// B, the rows of A, the step's first reduction index and the reduction's end.
+// Steps past the last unit, of the rows past the last group and of an empty
+// reduction get kk = K, i.e. empty descriptors.
+struct GroupStep {
+  int64_t a, b;
+  int rows, kk, K;
+};
+
+template <bool ROWS>
+__device__ __forceinline__ GroupStep group_step(const GroupedParams& p, const StepCursor& c, bool ok) {
+  GroupStep s;
+  if constexpr (ROWS) {
+    const bool live = ok && c.b < p.groups;
+    s.a = (int64_t)c.base * p.lda;
+    s.b = live ? (int64_t)c.b * p.batch_b : 0;
+    s.rows = live ? c.count : c.row0 + 1;
+    s.K = p.K;
+    s.kk = live ? c.kt * 64 : p.K;
+  } else {
+    s.a = (int64_t)c.base * p.lda;
+    s.b = (int64_t)c.base * p.ldb;
+    s.rows = p.M;
+    s.K = c.count;
+    s.kk = ok ? c.kt * 64 : c.count;
+  }
+  return s;
+}

@@ -72,13 +72,15 @@ extern "C" {
 typedef enum {
   DPG_OK = 0,
   DPG_ERR_INVALID_ARG = 1, /* negative size, ld < cols, NULL pointer for non-empty data, bad enum */
-  DPG_ERR_UNSUPPORTED = 2, /* split_k outside 0..64, or a launch beyond the grid limit */
+  DPG_ERR_UNSUPPORTED = 2, /* split_k outside 0..64, a launch beyond the grid limit, or a size beyond an entry point's stated limits */
   DPG_ERR_ALIGNMENT = 3,   /* pointer / ld / contiguous extent not 16-byte compatible */
   DPG_ERR_WORKSPACE = 4,   /* workspace smaller than dpg_workspace_size() */
   DPG_ERR_HIP = 5          /* a kernel launch failed */
 } dpg_status;
 
-typedef enum { DPG_BF16 = 0, DPG_F32 = 1 } dpg_dtype;
+/* DPG_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, no infinities)
+ * is a type of optimizer moments only. */
+typedef enum { DPG_BF16 = 0, DPG_F32 = 1, DPG_E4M3 = 2 } dpg_dtype;
 
 /* Passes; the short names (DPG_FWD ...) are aliases of the long ones. */
 typedef enum {
@@ -298,6 +300,143 @@ dpg_status dpg_plan_describe(dpg_pass pass, int64_t T, int64_t N, int64_t K, dpg
 void dpg_clear_plan_cache(void);
 void dpg_plan_cache_stats(int64_t* entries, int64_t* generation);
 int64_t dpg_plan_cache_capacity(void);
+
+/*
+ * Grouped products: the projections of an expert layer.  The rows of the token
+ * side are sorted by expert; group e (of E) holds the rows [offsets[e],
+ * offsets[e + 1]) and has its own weight matrix at w + e * stride_w.
+ *   forward: y[r, N]  = x[r, K] . w[e][N, K]^T           r in group e
+ *   dgrad  : dx[r, K] = dy[r, N] . w[e][N, K]
+ *   wgrad  : dw[e][N, K] = sum over the group's rows of dy[r, N]^T . x[r, K]
+ * BF16 operands, FP32 accumulation, BF16 or FP32 outputs, as for the single
+ * entry points.
+ *   offsets : int32 [E + 1] on the DEVICE, ascending; offsets[0] is taken as 0.
+ *             The sizes need not be known on the host: a call never waits.
+ *             Groups may be empty (their weight gradient is zeros).  Offsets
+ *             outside [0, R] or descending give unspecified values in the
+ *             output, never an access outside the operands.
+ *   R       : rows of the token side.  Rows at offsets[E] and past it belong to
+ *             no group: they are not read, and their output rows are zeros.
+ *   stride_*: elements between groups' matrices, a multiple of 16 bytes (0: one
+ *             weight for all groups).  Weight gradients must not overlap
+ *             (stacked, or side by side in wider rows, as for the batched calls).
+ * The plan depends on the sizes alone, every output element is summed by one
+ * workgroup in ascending order of the reduction, and nothing uses atomics: the
+ * bits are the same on every call and on every MI355X.  No workspace.
+ * Row strides of x, dy and w below 2^22 elements, R, N, K below 2^31 - 512 and
+ * E below 2^24 (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an
+ * empty reduction writes zeros.
+ */
+dpg_status dpg_grouped_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, void* y,
+                               int64_t ldy, dpg_dtype y_dtype, const int32_t* offsets, int64_t E, int64_t R,
+                               int64_t N, int64_t K, hipStream_t stream);
+dpg_status dpg_grouped_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t stride_w, void* dx,
+                             int64_t lddx, dpg_dtype dx_dtype, const int32_t* offsets, int64_t E, int64_t R,
+                             int64_t N, int64_t K, hipStream_t stream);
+dpg_status dpg_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, void* dw, int64_t lddw,
+                             int64_t stride_dw, dpg_dtype dw_dtype, const int32_t* offsets, int64_t E, int64_t R,
+                             int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * Routing: the top_k experts of every token, their weights, and the stable
+ * order of the (token, slot) pairs by expert.
+ *   logits   : FP32 [T, E], row stride ldl (any value >= E)
+ *   experts  : int32 [T, top_k], by descending logit, ties to the lowest
+ *              expert.  A logit of -infinity masks its expert; a token with
+ *              fewer than top_k unmasked experts has -1 in its last slots.
+ *   weights  : FP32 [T, top_k]; with renormalize != 0 the softmax over the
+ *              chosen experts, else the softmax over all E at the chosen ones;
+ *              0 in unused slots.  A NaN logit is never chosen and makes the
+ *              token's weights NaN.
+ *   offsets  : int32 [E + 1], first row of each expert and, last, the number of
+ *              used slots: the grouped products' offsets
+ *   rows     : int32 [T * top_k], the flat slot token * top_k + slot at each
+ *              row, by (expert, slot); the unused slots follow in order
+ *   positions: int32 [T, top_k], the inverse: each slot's row
+ * Pointers are 4-byte aligned.  1 <= top_k <= min(E, 32), E <= 512, T * top_k
+ * below 2^31 (DPG_ERR_UNSUPPORTED beyond).  Workspace:
+ * dpg_route_workspace_size (0 up to 64 tokens, one launch).
+ */
+size_t dpg_route_workspace_size(int64_t T, int64_t E, int64_t top_k);
+dpg_status dpg_route(const float* logits, int64_t ldl, int64_t T, int64_t E, int64_t top_k, int renormalize,
+                     int32_t* experts, float* weights, int32_t* offsets, int32_t* rows, int32_t* positions,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the weights by the logits (experts, weights as dpg_route wrote
+ * them): dlogits[t, i] = q_i (g_i - sum_j q_j g_j), q the softmax that
+ * `renormalize` names and g = dweights at the chosen experts, 0 elsewhere. */
+dpg_status dpg_route_dgrad(const float* logits, int64_t ldl, const int32_t* experts, const float* weights,
+                           const float* dweights, float* dlogits, int64_t lddl, int64_t T, int64_t E, int64_t top_k,
+                           int renormalize, hipStream_t stream);
+
+/*
+ * Rows into expert order, and back.  positions [T, top_k] and offsets [E + 1]
+ * are dpg_route's; R rows on the sorted side (T * top_k for a whole route).
+ *   dispatch: xs[positions[t, j]] = x[t], zeros at rows >= offsets[E]
+ *   combine : y[t] = sum_j weights[t, j] ys[positions[t, j]] in FP32, ascending
+ *             j, over the slots with positions below offsets[E]; weights NULL
+ *             means 1, which is the gradient of dispatch
+ *   combine_dgrad: dys[positions[t, j]] = weights[t, j] dy[t] (zeros at rows >=
+ *             offsets[E]) and dweights[t, j] = <dy[t], ys[positions[t, j]]> (0
+ *             for unused slots), summed in FP32
+ * Matrices follow the conventions at the top (16-byte rows); BF16 or FP32, one
+ * type per call except that combine takes one for ys and one for y.  Positions
+ * outside [0, R) are left out.
+ */
+dpg_status dpg_dispatch(const void* x, int64_t ldx, const int32_t* positions, const int32_t* offsets, void* xs,
+                        int64_t ldxs, dpg_dtype dtype, int64_t T, int64_t R, int64_t H, int64_t E, int64_t top_k,
+                        hipStream_t stream);
+dpg_status dpg_combine(const void* ys, int64_t ldys, dpg_dtype ys_dtype, const int32_t* positions,
+                       const int32_t* offsets, const float* weights, void* y, int64_t ldy, dpg_dtype y_dtype,
+                       int64_t T, int64_t R, int64_t H, int64_t E, int64_t top_k, hipStream_t stream);
+dpg_status dpg_combine_dgrad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* positions,
+                             const int32_t* offsets, const float* weights, void* dys, int64_t lddys, float* dweights,
+                             dpg_dtype dtype, int64_t T, int64_t R, int64_t H, int64_t E, int64_t top_k,
+                             hipStream_t stream);
+
+/*
+ * One AdamW step over `count` tensors (an array on the HOST), in as few
+ * launches as 48 tensors each allow.  Per element, g being the gradient times
+ * *grad_scale (a device scalar, NULL: 1), in FP32:
+ *   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * param is FP32 and updated in place; `copy`, if not NULL, receives it rounded
+ * to BF16 (the weights the products read).  Gradients are BF16 or FP32, one
+ * type per call.  Moments, one type per call:
+ *   DPG_F32  : exp_avg holds m, exp_avg_sq holds v
+ *   DPG_E4M3 : exp_avg holds m, exp_avg_sq holds sqrt(v), as codes whose values
+ *              times the scale of their block of 256 consecutive elements
+ *              (avg_scale, sq_scale: ceil(numel / 256) FP32 powers of two) are
+ *              the moments.  Storing rounds at random between the neighbouring
+ *              codes, from `seed`, the tensor's place in the array and the
+ *              element's place alone: the same call gives the same bits, and a
+ *              caller changes the seed from step to step.  A positive sqrt(v)
+ *              is not rounded to 0.  Zero codes with any finite scale start.
+ * Tensors are contiguous; any element alignment is taken (16-byte aligned ones
+ * run wide), up to 2^35 elements each.  step >= 1, 0 <= beta < 1, lr, eps, weight_decay finite and >= 0,
+ * else DPG_ERR_INVALID_ARG.  lr and step are host values: a captured call
+ * repeats them.
+ */
+typedef struct {
+  float* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* avg_scale;
+  float* sq_scale;
+  void* copy;
+  int64_t numel;
+} dpg_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const float* grad_scale;
+  dpg_dtype grad_dtype, state_dtype;
+  uint32_t seed;
+} dpg_adamw_options;
+dpg_status dpg_adamw(const dpg_adamw_tensor* tensors, int64_t count, const dpg_adamw_options* options,
+                     hipStream_t stream);
 
 /* Static text for a status code ("unknown status" for other values); the
  * error classes follow the validation rules above. */
