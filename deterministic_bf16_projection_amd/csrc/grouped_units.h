@@ -17,7 +17,9 @@
 //
 // The offsets come from device memory unseen by the host: every use clamps
 // them to [0, rows] and a group's end to its start or later, so wrong ones
-// give wrong results but no access outside the matrices.
+// give wrong results but no access outside the matrices.  Offsets that descend
+// would let groups overlap and the sum of their units pass 32 bits, so forward
+// and input gradient write nothing then.
 //
 // Included by gemm_fast.h inside namespace dpg.
 #pragma once
@@ -55,14 +57,17 @@ __device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) 
   m.per_lane = (p.groups + 63) >> 6;
   int units = 0;
   int at = 0;
+  bool ascending = true;
   const int g0 = lane * m.per_lane;
   if (g0 < p.groups) at = g0 == 0 ? 0 : min(max(p.offsets[g0], 0), p.rows);
   for (int i = 0; i < m.per_lane; ++i) {
     if (g0 + i >= p.groups) break;
     const int next = min(max(p.offsets[g0 + i + 1], 0), p.rows);
+    ascending &= next >= at;
     units += (max(next, at) - at + BM - 1) / BM;
     at = next;
   }
+  if (__ballot(!ascending) != 0) return m;  // no units
   units *= p.tiles_n;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
