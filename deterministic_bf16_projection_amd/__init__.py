@@ -22,8 +22,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdpg.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "dpg.h")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError("libdpg.so is not built; run `python deterministic_bf16_projection_amd/build.py` "
+if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_HERE, "_binding.so"))):
+    raise ImportError("libdpg.so and _binding.so are not built; run `python deterministic_bf16_projection_amd/build.py` "
                       "(or __graft_entry__.build()) first")
 
 _lib = ctypes.CDLL(LIB_PATH)
