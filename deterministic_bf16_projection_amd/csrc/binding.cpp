@@ -216,8 +216,19 @@ double number(PyObject* o, const char* name) {
   return v;
 }
 
+// the caller's workspace, or a new one of `need` bytes (undefined for none)
+Tensor workspace_of(PyObject* o, size_t need, const Tensor& like) {
+  if (o == Py_None) return need > 0 ? fresh({(int64_t)need}, at::kByte, like) : Tensor();
+  const Tensor& t = tensor(o, "workspace");
+  if (!t.is_cuda() || t.device() != like.device())
+    value_error("workspace must be a device tensor on " + like.device().str());
+  return t;
+}
+void* workspace_data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+size_t workspace_bytes(const Tensor& t) { return t.defined() ? t.nbytes() : 0; }
+
 // ---------------------------------------------------------------- entries --
-// forward (x, w), input gradient (dy, w): a, w, offsets, out, out_dtype
+// forward (x, w), input gradient (dy, w): a, w, offsets, out, out_dtype, workspace
 PyObject* grouped_rows(PyObject* const* a, bool forward) {
   const char* an = forward ? "x" : "dy";
   const Tensor& x = input(a[0], at::kBFloat16, an);
@@ -232,16 +243,19 @@ PyObject* grouped_rows(PyObject* const* a, bool forward) {
   const c10::DeviceGuard guard(x.device());
   Tensor out = output(a[3], {R, forward ? N : K}, dtype_of(a[4], at::kBFloat16), x);
   const Groups g = group_strides(w, "w");
+  const Tensor ws = workspace_of(
+      a[5], dpg_grouped_workspace_size(forward ? DPG_PASS_FORWARD : DPG_PASS_DGRAD, E, R, N, K), x);
   const auto fn = forward ? &dpg_grouped_forward : &dpg_grouped_dgrad;
   check_status(fn(x.data_ptr(), row_stride(x, an), w.data_ptr(), g.row, g.group, out.data_ptr(),
-                  row_stride(out, "out"), code_of(out.scalar_type()), data<int32_t>(off), E, R, N, K, stream_of(x)),
+                  row_stride(out, "out"), code_of(out.scalar_type()), data<int32_t>(off), E, R, N, K,
+                  workspace_data(ws), workspace_bytes(ws), stream_of(x)),
                forward ? "dpg_grouped_forward" : "dpg_grouped_dgrad");
   return wrap(std::move(out));
 }
 PyObject* grouped_forward(PyObject* const* a) { return grouped_rows(a, true); }
 PyObject* grouped_dgrad(PyObject* const* a) { return grouped_rows(a, false); }
 
-// dy, x, offsets, out, out_dtype
+// dy, x, offsets, out, out_dtype, workspace
 PyObject* grouped_wgrad(PyObject* const* a) {
   const Tensor& dy = input(a[0], at::kBFloat16, "dy");
   const Tensor& x = input(a[1], at::kBFloat16, "x");
@@ -254,9 +268,10 @@ PyObject* grouped_wgrad(PyObject* const* a) {
   const c10::DeviceGuard guard(dy.device());
   Tensor out = output(a[3], {E, N, K}, dtype_of(a[4], at::kBFloat16), dy);
   const Groups g = group_strides(out, "out");
+  const Tensor ws = workspace_of(a[5], dpg_grouped_workspace_size(DPG_PASS_WGRAD, E, R, N, K), dy);
   check_status(dpg_grouped_wgrad(dy.data_ptr(), row_stride(dy, "dy"), x.data_ptr(), row_stride(x, "x"),
                                  out.data_ptr(), g.row, g.group, code_of(out.scalar_type()), data<int32_t>(off), E, R,
-                                 N, K, stream_of(dy)),
+                                 N, K, workspace_data(ws), workspace_bytes(ws), stream_of(dy)),
                "dpg_grouped_wgrad");
   return wrap(std::move(out));
 }
@@ -284,14 +299,7 @@ PyObject* route(PyObject* const* a) {
   const size_t need = dpg_route_workspace_size(l.T, l.E, k);
   if (need == (size_t)-1) throw Status{1 <= k && k <= l.E ? DPG_ERR_UNSUPPORTED : DPG_ERR_INVALID_ARG, "dpg_route"};
   const c10::DeviceGuard guard(logits.device());
-  Tensor ws;
-  if (a[3] != Py_None) {
-    ws = tensor(a[3], "workspace");
-    if (!ws.is_cuda() || ws.device() != logits.device())
-      value_error("workspace must be a device tensor on " + logits.device().str());
-  } else if (need > 0) {
-    ws = fresh({(int64_t)need}, at::kByte, logits);
-  }
+  const Tensor ws = workspace_of(a[3], need, logits);
   const int64_t n = l.T * k;
   Block block(4 * Block::padded(4 * n) + Block::padded(4 * (l.E + 1)), logits);
   Tensor experts = block.part({l.T, k}, at::kInt), weights = block.part({l.T, k}, at::kFloat);
@@ -299,7 +307,7 @@ PyObject* route(PyObject* const* a) {
   Tensor positions = block.part({l.T, k}, at::kInt);
   check_status(dpg_route(data<float>(logits), l.ld, l.T, l.E, k, renorm, data<int32_t>(experts), data<float>(weights),
                          data<int32_t>(offsets), data<int32_t>(rows), data<int32_t>(positions),
-                         need ? ws.data_ptr() : nullptr, need ? ws.nbytes() : 0, stream_of(logits)),
+                         workspace_data(ws), workspace_bytes(ws), stream_of(logits)),
                "dpg_route");
   PyObject* r = PyTuple_New(5);
   if (!r) return nullptr;
@@ -534,9 +542,9 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 }
 
 #define ENTRY(name, n) {#name, (PyCFunction)(void (*)(void))&entry<&name, n>, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {ENTRY(grouped_forward, 5),
-                           ENTRY(grouped_dgrad, 5),
-                           ENTRY(grouped_wgrad, 5),
+PyMethodDef g_methods[] = {ENTRY(grouped_forward, 6),
+                           ENTRY(grouped_dgrad, 6),
+                           ENTRY(grouped_wgrad, 6),
                            ENTRY(route, 4),
                            ENTRY(route_dgrad, 6),
                            ENTRY(dispatch, 4),

@@ -4,9 +4,11 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "api_common.h"
 #include "gemm_fast.h"
+#include "grouped_skinny.h"
 
 namespace dpg {
 namespace {
@@ -23,9 +25,23 @@ struct GroupedRow {
 struct GroupedTile {
   int bm, bn, threads, per_cu;
 };
-constexpr GroupedTile kGroupedTiles[] = {{256, 256, 512, 1}, {128, 128, 256, 2}};
 
-GroupedFn lookup_grouped_kernel(int tile, int layout, int out) {
+// The variants: the large kernel's two tiles, then the few-row kernels (forward:
+// 64 rows by 16 columns or 32 by 32, input gradient: 16 by 128).
+enum Variant { TILE_256, TILE_128, ROWS_64X16, ROWS_32X32, ROWS_16X128 };
+constexpr GroupedTile kGroupedTiles[] = {
+    {256, 256, 512, 1}, {128, 128, 256, 2}, {64, 16, 512, 2}, {32, 32, 512, 2}, {16, 128, 512, 2}};
+
+template <int OUT>
+GroupedFn lookup_skinny_kernel(int variant) {
+  return variant == ROWS_64X16   ? &grouped_skinny_kernel<false, 4, 1, 4, OUT>
+         : variant == ROWS_32X32 ? &grouped_skinny_kernel<false, 2, 2, 3, OUT>
+                                 : &grouped_skinny_kernel<true, 1, 8, 1, OUT>;
+}
+
+GroupedFn lookup_grouped_kernel(int variant, int layout, int out) {
+  if (variant >= ROWS_64X16)
+    return out == DPG_F32 ? lookup_skinny_kernel<OUT_F32>(variant) : lookup_skinny_kernel<OUT_BF16>(variant);
   static const GroupedFn table[2][3][2] = {
       {{GroupedRow<256, 256, 2, 4, 0>::fns[0], GroupedRow<256, 256, 2, 4, 0>::fns[1]},
        {GroupedRow<256, 256, 2, 4, 1>::fns[0], GroupedRow<256, 256, 2, 4, 1>::fns[1]},
@@ -33,20 +49,95 @@ GroupedFn lookup_grouped_kernel(int tile, int layout, int out) {
       {{GroupedRow<128, 128, 2, 2, 0>::fns[0], GroupedRow<128, 128, 2, 2, 0>::fns[1]},
        {GroupedRow<128, 128, 2, 2, 1>::fns[0], GroupedRow<128, 128, 2, 2, 1>::fns[1]},
        {GroupedRow<128, 128, 2, 2, 2>::fns[0], GroupedRow<128, 128, 2, 2, 2>::fns[1]}}};
-  return table[tile][layout][out];
+  return table[variant][layout][out];
 }
 
-// 256x256 tiles where the average group fills them, 128x128 otherwise.
-int grouped_tile(int layout, int64_t R, int64_t E, int64_t M, int64_t N) {
-  if (layout == LAYOUT_WGRAD) return M >= 256 && N >= 256 ? 0 : 1;
-  return R >= 192 * E && N >= 256 ? 0 : 1;
+struct GroupedPlan {
+  int variant, splits;
+};
+
+// The plan with the least estimated time, from the sizes alone (a CU count of
+// 256 whatever the device, so that the bits do not depend on it).  The
+// estimates are fitted to 470 timings of 80 sizes on an MI355X (64 to 2048 by
+// 128 to 4096, 1 to 256 groups, 1 to 65536 rows, each with every variant and 1
+// to 16 splits): the choice is 1.6% slower than the best one on average, where
+// always the best unsplit tile of the two is 1.9 times slower.  In us:
+//   tiles: a unit takes its steps of 64 (about 1 while few units run; more when
+//     they share the chip) and its epilogue; splitting adds a launch and the
+//     traffic of its planes.  For example a weight gradient of 30000 rows into
+//     512 x 512: 438 in 128-tiles, 40 with 16 splits; a forward of 1024 rows
+//     and 8 groups, 1024 x 4096: 66 and 33 with 4.
+//   few rows: each CU moves 38 GB/s (forward) or 72 (input gradient) through
+//     its unit's fragments.  A forward of 8 rows in 8 of 256 groups, 512 x
+//     4096: 11, in 128-tiles 65.
+// A weight gradient's longest group is taken to hold 1.3 times the mean.
+GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K) {
+  GroupedPlan best = {TILE_128, 1};
+  if (E == 0 || R == 0 || N == 0 || K == 0) return best;
+  constexpr double kCus = kDetCus, kStart = 4.6;  // us
+  // bytes of weights per us from memory: tiles of the forward (fetched into
+  // LDS) and of the input gradient, and the few-row kernels
+  const double tile_rate = layout == LAYOUT_FWD ? 4.6e6 : 5.4e6, rows_rate = 5.1e6;
+  const bool wgrad = layout == LAYOUT_WGRAD;
+  const double groups = (double)std::min(E, R);  // with rows
+  const double cols = (double)(layout == LAYOUT_FWD ? N : K), weights = groups * (double)N * (double)K * 2;
+  const double reduced = wgrad ? 1.3 * (double)R / (double)E : (double)(layout == LAYOUT_FWD ? K : N);
+  const double outputs = wgrad ? (double)E * (double)N * (double)K : (double)R * cols;
+  const auto row_tiles = [&](double bm) {
+    const double few = std::max(groups, std::ceil((double)R / bm));
+    return (double)R / groups > bm / 4 ? std::max(std::ceil((double)R / bm), (double)R / bm + 0.5 * groups) : few;
+  };
+  static constexpr double kStepAlone[3][2] = {{1.0, 0.64}, {1.11, 0.78}, {0.81, 0.67}};
+  static constexpr double kStepFull[3][2] = {{1.61, 1.09}, {1.04, 0.97}, {1.65, 1.17}};
+  static constexpr double kEpilogue[2] = {5.0, 2.9};
+  double least = 0;
+  for (int v = TILE_256; v <= TILE_128; ++v) {
+    const GroupedTile& t = kGroupedTiles[v];
+    const double slots = kCus * t.per_cu;
+    const double tiles = wgrad ? (double)E * std::ceil((double)N / t.bm) * std::ceil((double)K / t.bn)
+                               : row_tiles(t.bm) * std::ceil(cols / t.bn);
+    const double steps = std::ceil(reduced / 64);
+    for (int s = 1; s <= 16; s *= 2) {
+      if (s > 1 && (s > steps || s * outputs * 4 > (double)(1ll << 30))) break;
+      const double rounds = tiles * s / slots, load = std::min(1.0, rounds);
+      const double step = kStepAlone[layout][v] + (kStepFull[layout][v] - kStepAlone[layout][v]) * load;
+      double us = kStart + (rounds < 3 ? std::max(1.0, std::ceil(rounds)) : rounds + 0.5) *
+                               (std::ceil(steps / s) * step + kEpilogue[v]);
+      if (!wgrad) us = std::max(us, kStart + weights / tile_rate);
+      if (s > 1) us += 1.8 + (s + 1) * outputs * 4 / 4.55e6;
+      if (least == 0 || us < least) {
+        least = us;
+        best = {v, s};
+      }
+    }
+  }
+  for (int v = ROWS_64X16; v <= ROWS_16X128 && !wgrad; ++v) {
+    if ((v == ROWS_16X128) != (layout == LAYOUT_DGRAD)) continue;
+    const GroupedTile& t = kGroupedTiles[v];
+    const double tiles = row_tiles(t.bm);
+    const double rows = std::min((double)t.bm, std::ceil((double)R / tiles));
+    const double bytes = reduced * 2 * (rows + t.bn) + 26e3, rate = layout == LAYOUT_FWD ? 38e3 : 72e3;
+    const double us = kStart + std::max(std::max(tiles * std::ceil(cols / t.bn) / kCus, 1.0) * bytes / rate,
+                                        weights / rows_rate);
+    if (us < least) {
+      least = us;
+      best = {v, 1};
+    }
+  }
+  return best;
+}
+
+size_t grouped_workspace(int layout, const GroupedPlan& plan, int64_t E, int64_t R, int64_t N, int64_t K) {
+  if (plan.splits == 1) return 0;
+  const int64_t elements = layout == LAYOUT_FWD ? R * N : layout == LAYOUT_DGRAD ? R * K : E * N * K;
+  return (size_t)plan.splits * (size_t)elements * sizeof(float);
 }
 
 // One grouped pass.  (a, b) are (x, w), (dy, w) and (dy, x); `stride` is the
 // element stride between the groups' weights (weight gradient: outputs).
 dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, int64_t ldb, void* c, int64_t ldc,
                        int64_t stride, int out, const int32_t* offsets, int64_t E, int64_t R, int64_t N, int64_t K,
-                       hipStream_t stream) {
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (out != DPG_BF16 && out != DPG_F32) return DPG_ERR_INVALID_ARG;
   if (E < 0 || R < 0 || N < 0 || K < 0 || stride < 0) return DPG_ERR_INVALID_ARG;
   const int out_elt = out == DPG_F32 ? 4 : 2;
@@ -93,20 +184,41 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   p.offsets = offsets;
   p.groups = (int)E;
   p.rows = (int)R;
-  const int tile = grouped_tile(layout, R, E, p.M, p.N);
-  const GroupedTile& t = kGroupedTiles[tile];
+  const GroupedPlan plan = grouped_plan(layout, E, R, N, K);
+  const GroupedTile& t = kGroupedTiles[plan.variant];
   p.tiles_m = (p.M + t.bm - 1) / t.bm;
   p.tiles_n = (p.N + t.bn - 1) / t.bn;
   p.kt_total = std::max(1, (p.K + 63) / 64);
   p.group_m = 4;
+  p.splits = plan.splits;
   // the most units there can be: every group with rows may end in a part of a
   // tile, and so may the rows past the last group
   const int64_t tiles_m = wgrad ? E * p.tiles_m : R / t.bm + std::min<int64_t>(E + 1, R);
-  const int64_t units = tiles_m * p.tiles_n;
+  const int64_t units = tiles_m * p.tiles_n * p.splits;
   if (units >= (1ll << 31) - (1 << 20)) return DPG_ERR_UNSUPPORTED;
   const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus() * t.per_cu);
   void* args[] = {&p};
-  return launch((const void*)lookup_grouped_kernel(tile, layout, out), grid, t.threads, 0, args, stream);
+  if (p.splits == 1)
+    return launch((const void*)lookup_grouped_kernel(plan.variant, layout, out), grid, t.threads, 0, args, stream);
+  // the splits' sums go to planes of the workspace: [splits][R][cols], or
+  // [E][splits][N][K] of the weight gradient
+  if (!workspace || workspace_bytes < grouped_workspace(layout, plan, E, R, N, K) || !aligned16(workspace))
+    return DPG_ERR_WORKSPACE;
+  p.c = workspace;
+  p.ldc = p.N;
+  p.split_stride = (int64_t)p.M * p.N;
+  p.batch_c = p.split_stride * p.splits;
+  st = launch((const void*)lookup_grouped_kernel(plan.variant, layout, DPG_F32), grid, t.threads, 0, args, stream);
+  if (st != DPG_OK) return st;
+  const float* ws = (const float*)workspace;
+  int64_t batch = wgrad ? E : 1;
+  const int gx = (p.N / 4 + 255) / 256;
+  const int gy = (int)std::max<int64_t>(1, std::min<int64_t>(batch * p.M, std::max(1, 2048 / gx)));
+  void* rargs[] = {&ws, &p.splits, &p.split_stride, &p.M, &p.N, &c, &ldc, &batch, &stride};
+  const hipError_t e = hipLaunchKernel(out == DPG_F32 ? (const void*)&splitk_reduce_kernel<OUT_F32>
+                                                      : (const void*)&splitk_reduce_kernel<OUT_BF16>,
+                                       dim3(gx, gy), dim3(256), rargs, 0, stream);
+  return e == hipSuccess ? DPG_OK : DPG_ERR_HIP;
 }
 
 }  // namespace
@@ -116,23 +228,31 @@ using namespace dpg;
 
 extern "C" {
 
+size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K) {
+  const int layout = (int)pass;
+  if (layout < LAYOUT_FWD || layout > LAYOUT_WGRAD || E < 0 || R < 0 || N < 0 || K < 0) return (size_t)-1;
+  return grouped_workspace(layout, grouped_plan(layout, E, R, N, K), E, R, N, K);
+}
+
 dpg_status dpg_grouped_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, void* y,
                                int64_t ldy, dpg_dtype y_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                               int64_t N, int64_t K, hipStream_t stream) {
-  return run_grouped(LAYOUT_FWD, x, ldx, w, ldw, y, ldy, stride_w, (int)y_dtype, offsets, E, R, N, K, stream);
+                               int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return run_grouped(LAYOUT_FWD, x, ldx, w, ldw, y, ldy, stride_w, (int)y_dtype, offsets, E, R, N, K, workspace,
+                     workspace_bytes, stream);
 }
 
 dpg_status dpg_grouped_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t stride_w, void* dx,
                              int64_t lddx, dpg_dtype dx_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                             int64_t N, int64_t K, hipStream_t stream) {
-  return run_grouped(LAYOUT_DGRAD, dy, lddy, w, ldw, dx, lddx, stride_w, (int)dx_dtype, offsets, E, R, N, K, stream);
+                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return run_grouped(LAYOUT_DGRAD, dy, lddy, w, ldw, dx, lddx, stride_w, (int)dx_dtype, offsets, E, R, N, K, workspace,
+                     workspace_bytes, stream);
 }
 
 dpg_status dpg_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, void* dw, int64_t lddw,
                              int64_t stride_dw, dpg_dtype dw_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                             int64_t N, int64_t K, hipStream_t stream) {
+                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   return run_grouped(LAYOUT_WGRAD, dy, lddy, x, ldx, dw, lddw, stride_dw, (int)dw_dtype, offsets, E, R, N, K,
-                     stream);
+                     workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

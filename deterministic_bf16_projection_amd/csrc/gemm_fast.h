@@ -579,11 +579,11 @@ struct FastGemm {
                                                   f32x16 (&acc)[FM][FN], char* scr) {
     char* out;
     if constexpr (GR_ROWS) {
-      out = (char*)p.c + (int64_t)c.base * p.ldc * (OUT == OUT_BF16 ? 2 : 4);
+      out = (char*)p.c + ((int64_t)c.base * p.ldc + (int64_t)c.split * p.split_stride) * (OUT == OUT_BF16 ? 2 : 4);
       store_tile<OUT>(out, p.ldc, 0, 0, c.count, p.N, c.row0, c.col0, lane, wm, wn, acc, scr);
       return;
     }
-    if (OUT == OUT_PARTIAL)
+    if (OUT == OUT_PARTIAL || (GR && OUT == OUT_F32))
       out = (char*)p.c + ((int64_t)c.b * p.batch_c + (int64_t)c.split * p.split_stride) * 4;
     else
       out = (char*)p.c + (int64_t)c.b * p.batch_c * (OUT == OUT_BF16 ? 2 : 4);

@@ -51,7 +51,7 @@ template <int BM, bool ROWS>
 __device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) {
   GroupMap m = {};
   if constexpr (!ROWS) {
-    m.total = m.grouped = p.groups * p.tiles_m * p.tiles_n;
+    m.total = m.grouped = p.groups * p.tiles_m * p.tiles_n * p.splits;
     return m;
   }
   m.per_lane = (p.groups + 63) >> 6;
@@ -59,13 +59,19 @@ __device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) 
   int at = 0;
   bool ascending = true;
   const int g0 = lane * m.per_lane;
-  if (g0 < p.groups) at = g0 == 0 ? 0 : min(max(p.offsets[g0], 0), p.rows);
-  for (int i = 0; i < m.per_lane; ++i) {
-    if (g0 + i >= p.groups) break;
-    const int next = min(max(p.offsets[g0 + i + 1], 0), p.rows);
-    ascending &= next >= at;
-    units += (max(next, at) - at + BM - 1) / BM;
-    at = next;
+  if (p.groups > 0 && g0 > 0) at = min(max(p.offsets[min(g0, p.groups)], 0), p.rows);
+  for (int i0 = 0; p.groups > 0 && i0 < m.per_lane; i0 += 4) {
+    int next[4];  // four loads in flight
+#pragma unroll
+    for (int i = 0; i < 4; ++i) next[i] = p.offsets[min(g0 + i0 + i + 1, p.groups)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= m.per_lane || g0 + i0 + i >= p.groups) continue;
+      const int end = min(max(next[i], 0), p.rows);
+      ascending &= end >= at;
+      units += (max(end, at) - at + BM - 1) / BM;
+      at = end;
+    }
   }
   if (__ballot(!ascending) != 0) return m;  // no units
   units *= p.tiles_n;
@@ -78,8 +84,21 @@ __device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) 
   m.grouped = __builtin_amdgcn_readlane(units, 63);
   const const_int_t* o = (const const_int_t*)(uintptr_t)p.offsets;
   m.tail0 = p.groups == 0 ? 0 : min(max(o[p.groups], 0), p.rows);
-  m.total = m.grouped + (p.rows - m.tail0 + BM - 1) / BM * p.tiles_n;
+  m.total = (m.grouped + (p.rows - m.tail0 + BM - 1) / BM * p.tiles_n) * p.splits;
   return m;
+}
+
+// The K tiles of the unit's split, at least one (which reads zeros).
+__device__ __forceinline__ void group_split(const GroupedParams& p, StepCursor& c, int k_tiles) {
+  if (p.splits > 1) {
+    const SplitParts sp = split_parts(p.splits, k_tiles);
+    c.kt0 = split_begin(c.split, sp);
+    c.nkt = max(1, split_begin(c.split + 1, sp) - c.kt0);
+    // an empty split starts past the reduction
+    if (split_begin(c.split + 1, sp) == c.kt0) c.kt0 = k_tiles;
+  } else {
+    c.nkt = max(1, k_tiles);
+  }
 }
 
 // Unit u of the stream: the units of one group are consecutive, rastered in
@@ -90,7 +109,12 @@ __device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const
   StepCursor c;
   c.u = unit;
   c.kt = c.kt0 = c.split = 0;
-  const int id = __builtin_amdgcn_readfirstlane(xcd_remap(min(unit, m.total - 1), m.total));
+  int id = __builtin_amdgcn_readfirstlane(xcd_remap(min(unit, m.total - 1), m.total));
+  if (p.splits > 1) {
+    const int per_split = m.total / p.splits;
+    c.split = id / per_split;
+    id -= c.split * per_split;
+  }
   int t, tiles_m;
   if constexpr (ROWS) {
     const int l = __builtin_popcountll(__ballot(m.lane_end <= id));
@@ -106,7 +130,7 @@ __device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const
         t -= tiles_m * p.tiles_n;
         ++c.b;
       }
-      c.nkt = p.kt_total;
+      group_split(p, c, p.kt_total);
     } else {
       t = id - m.grouped;
       c.b = p.groups;
@@ -122,7 +146,7 @@ __device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const
     group_rows(p.offsets, p.rows, c.b, c.base, end);
     c.count = end - c.base;
     tiles_m = p.tiles_m;
-    c.nkt = max(1, (c.count + 63) >> 6);
+    group_split(p, c, (c.count + 63) >> 6);
   }
   const int per_band = p.group_m * p.tiles_n;
   const int band = t / per_band;
@@ -152,13 +176,13 @@ __device__ __forceinline__ GroupStep group_step(const GroupedParams& p, const St
     s.b = live ? (int64_t)c.b * p.batch_b : 0;
     s.rows = live ? c.count : c.row0 + 1;
     s.K = p.K;
-    s.kk = live ? c.kt * 64 : p.K;
+    s.kk = live ? min((c.kt0 + c.kt) * 64, p.K) : p.K;
   } else {
     s.a = (int64_t)c.base * p.lda;
     s.b = (int64_t)c.base * p.ldb;
     s.rows = p.M;
     s.K = c.count;
-    s.kk = ok ? c.kt * 64 : c.count;
+    s.kk = ok ? min((c.kt0 + c.kt) * 64, c.count) : c.count;
   }
   return s;
 }

@@ -38,28 +38,28 @@ def _on(stream, tensor, fn, *args):
 
 
 # ------------------------------------------------------- grouped products --
-def dpg_grouped_forward(x, w, offsets, out=None, out_dtype=torch.bfloat16, stream=None):
+def dpg_grouped_forward(x, w, offsets, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """y[r] = x[r] w[e]^T for the rows r of group e, offsets[e] <= r <
     offsets[e + 1]: x [R, K] BF16 sorted by group, w [E, N, K] BF16, offsets
     int32 [E + 1] on the device.  Rows from offsets[E] on give zeros."""
     if stream is None:
-        return _binding.grouped_forward(x, w, offsets, out, out_dtype)
-    return _on(stream, x, _binding.grouped_forward, x, w, offsets, out, out_dtype)
+        return _binding.grouped_forward(x, w, offsets, out, out_dtype, workspace)
+    return _on(stream, x, _binding.grouped_forward, x, w, offsets, out, out_dtype, workspace)
 
 
-def dpg_grouped_dgrad(dy, w, offsets, out=None, out_dtype=torch.bfloat16, stream=None):
+def dpg_grouped_dgrad(dy, w, offsets, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """dx[r] = dy[r] w[e] for the rows r of group e: dy [R, N], w [E, N, K]."""
     if stream is None:
-        return _binding.grouped_dgrad(dy, w, offsets, out, out_dtype)
-    return _on(stream, dy, _binding.grouped_dgrad, dy, w, offsets, out, out_dtype)
+        return _binding.grouped_dgrad(dy, w, offsets, out, out_dtype, workspace)
+    return _on(stream, dy, _binding.grouped_dgrad, dy, w, offsets, out, out_dtype, workspace)
 
 
-def dpg_grouped_wgrad(dy, x, offsets, out=None, out_dtype=torch.bfloat16, stream=None):
+def dpg_grouped_wgrad(dy, x, offsets, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """dw[e] = sum over the rows r of group e of dy[r]^T x[r], as [E, N, K]: dy
     [R, N], x [R, K].  A group without rows gives zeros."""
     if stream is None:
-        return _binding.grouped_wgrad(dy, x, offsets, out, out_dtype)
-    return _on(stream, dy, _binding.grouped_wgrad, dy, x, offsets, out, out_dtype)
+        return _binding.grouped_wgrad(dy, x, offsets, out, out_dtype, workspace)
+    return _on(stream, dy, _binding.grouped_wgrad, dy, x, offsets, out, out_dtype, workspace)
 
 
 # ---------------------------------------------------------------- routing --

@@ -320,22 +320,25 @@ int64_t dpg_plan_cache_capacity(void);
  *   stride_*: elements between groups' matrices, a multiple of 16 bytes (0: one
  *             weight for all groups).  Weight gradients must not overlap
  *             (stacked, or side by side in wider rows, as for the batched calls).
- * The plan depends on the sizes alone, every output element is summed by one
- * workgroup in ascending order of the reduction, and nothing uses atomics: the
- * bits are the same on every call and on every MI355X.  No workspace.
+ * The plan depends on the sizes and the device's CU count alone, every sum runs
+ * in a fixed order and nothing uses atomics: the bits are the same on every
+ * call and on every MI355X.  Where there are few output tiles the reduction is
+ * split (each group's rows, for wgrad) and the parts are added in order from
+ * the workspace: dpg_grouped_workspace_size bytes, 0 where nothing is split.
  * Row strides of x, dy and w below 2^22 elements, R, N, K below 2^31 - 512 and
  * E below 2^24 (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an
  * empty reduction writes zeros.
  */
+size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K);
 dpg_status dpg_grouped_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, void* y,
                                int64_t ldy, dpg_dtype y_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                               int64_t N, int64_t K, hipStream_t stream);
+                               int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream);
 dpg_status dpg_grouped_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t stride_w, void* dx,
                              int64_t lddx, dpg_dtype dx_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                             int64_t N, int64_t K, hipStream_t stream);
+                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream);
 dpg_status dpg_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, void* dw, int64_t lddw,
                              int64_t stride_dw, dpg_dtype dw_dtype, const int32_t* offsets, int64_t E, int64_t R,
-                             int64_t N, int64_t K, hipStream_t stream);
+                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Routing: the top_k experts of every token, their weights, and the stable

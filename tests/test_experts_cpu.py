@@ -16,9 +16,10 @@ I, Z = ctypes.c_int64, ctypes.c_size_t
 
 def _grouped(name, a=P, lda=64, b=P, ldb=64, stride=4096, c=P, ldc=64, dtype=0, offsets=P, E=4, R=10, N=64, K=64):
     if name == "wgrad":
-        args = (a, I(lda), b, I(ldb), c, I(ldc), I(stride), dtype, offsets, I(E), I(R), I(N), I(K), None)
+        args = (a, I(lda), b, I(ldb), c, I(ldc), I(stride), dtype, offsets, I(E), I(R), I(N), I(K), P, Z(1 << 40), None)
     else:
-        args = (a, I(lda), b, I(ldb), I(stride), c, I(ldc), dtype, offsets, I(E), I(R), I(N), I(K), None)
+        args = (a, I(lda), b, I(ldb), I(stride), c, I(ldc), dtype, offsets, I(E), I(R), I(N), I(K), P, Z(1 << 40),
+                None)
     return getattr(dpg.lib(), "dpg_grouped_" + name)(*args)
 
 

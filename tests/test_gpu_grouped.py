@@ -2,6 +2,8 @@
 exact in FP32 make the comparison with the 64-bit product bit for bit: FP32
 outputs equal it, BF16 outputs are its nearest-even rounding.  Memory that a
 call must not read holds NaN, memory that it must not write a sentinel."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -231,6 +233,39 @@ def test_reruns_streams_and_graph_replays_are_bitwise_equal(pass_):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, fn(a, b, off))
+
+
+def _workspace(pass_, E, R, N, K):
+    fn = dpg.lib().dpg_grouped_workspace_size
+    fn.argtypes, fn.restype = [ctypes.c_int] + [ctypes.c_int64] * 4, ctypes.c_size_t
+    return fn(PASSES.index(pass_), E, R, N, K)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pass_,counts,N,K,tail,split", [
+    ("forward", [700, 0, 300], 520, 4096, 0, True), ("forward", [700, 90], 1024, 2056, 33, True),
+    ("dgrad", [3000, 0, 900], 4096, 520, 0, True), ("dgrad", [2500], 2056, 264, 70, True),
+    ("wgrad", [3000], 264, 136, 0, True), ("wgrad", [2000, 0, 5, 1700], 520, 264, 40, True),
+    ("forward", [1, 0, 3, 0, 2], 1024, 4096, 5, False), ("forward", [16, 17, 33, 64, 65], 520, 2056, 9, False),
+    ("dgrad", [1, 0, 3, 0, 2], 1024, 4096, 5, False), ("dgrad", [16, 17, 33], 520, 2056, 9, False)])
+def test_split_reductions_and_few_rows(pass_, counts, N, K, tail, split, out_dtype):
+    """Long reductions of few output tiles are split; the few-row kernels take
+    what their row tiles do not fill.  Sums below 2^24: exact."""
+    assert (_workspace(pass_, len(counts), sum(counts) + tail, N, K) > 0) == split
+    _check(pass_, counts, N, K, out_dtype, tail=tail, pad=8)
+
+
+def test_workspace():
+    g = np.random.default_rng(10)
+    dy, x, off = _ints(g, 3000, 264), _ints(g, 3000, 136), _offsets([3000])
+    need = _workspace("wgrad", 1, 3000, 264, 136)
+    first = dpg.dpg_grouped_wgrad(dy, x, off)
+    own = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(dpg.dpg_grouped_wgrad(dy, x, off, workspace=own), first)
+    with pytest.raises(dpg.DpgError):
+        dpg.dpg_grouped_wgrad(dy, x, off, workspace=own[:need - 16])
+    with pytest.raises(ValueError):
+        dpg.dpg_grouped_wgrad(dy, x, off, workspace=own.cpu())
 
 
 def test_refusals():
