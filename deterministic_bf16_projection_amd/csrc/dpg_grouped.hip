@@ -197,6 +197,8 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   const int64_t units = tiles_m * p.tiles_n * p.splits;
   if (units >= (1ll << 31) - (1 << 20)) return DPG_ERR_UNSUPPORTED;
   const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus() * t.per_cu);
+  // worth its microsecond where a workgroup takes several groups' units
+  p.ordered = wgrad && E <= kOrderGroups && E > 1 && units > grid;
   void* args[] = {&p};
   if (p.splits == 1)
     return launch((const void*)lookup_grouped_kernel(plan.variant, layout, out), grid, t.threads, 0, args, stream);

@@ -655,7 +655,8 @@ struct FastGemm {
     }
   }
 
-  static __device__ __forceinline__ void run(__bf16* smem, const Params& p, int ltid, int lane, int wm, int wn) {
+  static __device__ __forceinline__ void run(__bf16* smem, const Params& p, int ltid, int lane, int wm, int wn,
+                                             unsigned group_order = 0) {
     // this wave's epilogue buffer, after the two pipeline stages
     char* scr = (char*)(smem + 2 * STAGE) + (wm * WAVES_N + wn) * 4096;
     const InT* A = (const InT*)p.a;
@@ -679,7 +680,11 @@ struct FastGemm {
                         p.tiles_m * p.tiles_n * p.splits, split_parts(p.splits, p.kt_total)};
     const int stride = gridDim.x;
     GroupMap gm = {};
-    if constexpr (GR) gm = group_map<BM, GR_ROWS>(p, lane);
+    if constexpr (GR) {
+      gm = group_map<BM, GR_ROWS>(p, lane);
+      gm.order = group_order;
+      gm.place = xcd_remap(blockIdx.x, gridDim.x);
+    }
     // the workgroup's unit stream: (tile, K split) units, its stream-K work, or
     // (group, tile) units
     auto first_step = [&]() -> StepCursor {
@@ -706,7 +711,7 @@ struct FastGemm {
     };
     auto valid = [&](const StepCursor& c) -> bool {
       if constexpr (GR)
-        return c.u < gm.total;
+        return c.u >= 0;
       else
         return cursor_valid(um, c);
     };
@@ -1008,13 +1013,17 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1)
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: SGPR
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  unsigned order = 0;
+  if constexpr (GR && !A_KMAJ) {
+    if (p.ordered) order = group_order<NT>(p, tid, (int*)smem);
+  }
   if constexpr (NT == 512) {
     if (wave < 4)
-      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_A, false, SK, GR>::run(smem, p, tid, lane, wm, wn);
+      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_A, false, SK, GR>::run(smem, p, tid, lane, wm, wn, order);
     else
-      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_B, false, SK, GR>::run(smem, p, tid - 256, lane, wm, wn);
+      FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_B, false, SK, GR>::run(smem, p, tid - 256, lane, wm, wn, order);
   } else {
-    FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_BOTH, X3, SK, GR>::run(smem, p, tid, lane, wm, wn);
+    FastGemm<BM, BN, WAVES_M, WAVES_N, A_KMAJ, B_KMAJ, OUT, ROLE_BOTH, X3, SK, GR>::run(smem, p, tid, lane, wm, wn, order);
   }
 }
 

@@ -28,6 +28,7 @@ struct GroupedParams : GemmParams {
   const int* offsets;  // groups + 1, on the device; offsets[0] is taken as 0
   int groups;
   int rows;            // rows of the token-side matrices
+  int ordered;         // weight gradient: groups by descending size
 };
 
 typedef __attribute__((address_space(4))) const int const_int_t;
@@ -39,13 +40,60 @@ __device__ __forceinline__ void group_rows(const int* offsets, int rows, int g, 
   end = min(max(o[g + 1], first), rows);
 }
 
+// Weight gradient: a workgroup's units should take equally long in sum, and
+// the groups' sizes differ (by 15 times among 64 groups of a skewed router).
+// The groups are taken by descending size, each round of the grid going
+// through the workgroups in the opposite direction of the one before, so that
+// the large and small ones of neighbouring rounds even out.  The order of up
+// to kOrderGroups groups is found at the start of every workgroup: each thread
+// counts the groups before its own, and lane l of a wave keeps the four groups
+// of ranks 4 l .. 4 l + 3 in one register.
+constexpr int kOrderGroups = 256;
+
 struct GroupMap {
   int per_lane;   // groups of one lane
   int lane_end;   // units of this lane's groups and all before (one value per lane)
   int grouped;    // units of all groups
   int total;      // with those of the rows past the last group
   int tail0;      // first row past the last group
+  unsigned order; // weight gradient: four groups by rank
+  int place;      // weight gradient: this workgroup's place in a round
 };
+
+// `scratch`: (NT + 64) dwords of LDS, free until the call returns
+template <int NT>
+__device__ __forceinline__ unsigned group_order(const GroupedParams& p, int tid, int* scratch) {
+  constexpr int SHARE = NT / kOrderGroups;  // threads of one group
+  int* count = scratch;                     // kOrderGroups
+  unsigned char* ranked = (unsigned char*)(scratch + NT);
+  const int g = tid % kOrderGroups, part = tid / kOrderGroups;
+  if (tid < kOrderGroups) {
+    int n = -1;
+    if (g < p.groups) {
+      const int first = g == 0 ? 0 : min(max(p.offsets[g], 0), p.rows);
+      n = max(min(max(p.offsets[g + 1], 0), p.rows) - first, 0);
+    }
+    count[g] = n;
+    if (SHARE > 1) count[kOrderGroups + g] = 0;
+  }
+  __syncthreads();
+  const int mine = count[g];
+  int before = 0;
+  for (int o = part * (kOrderGroups / SHARE); o < min(p.groups, (part + 1) * (kOrderGroups / SHARE)); ++o) {
+    const int n = count[o];
+    before += n > mine || (n == mine && o < g);
+  }
+  if (SHARE > 1) {
+    atomicAdd(&count[kOrderGroups + g], before);
+    __syncthreads();
+    before = count[kOrderGroups + g];
+  }
+  if (tid < kOrderGroups && g < p.groups) ranked[before] = (unsigned char)g;
+  __syncthreads();
+  const unsigned order = ((const unsigned*)ranked)[tid & 63];
+  __syncthreads();  // the LDS becomes the pipeline's
+  return order;
+}
 
 template <int BM, bool ROWS>
 __device__ __forceinline__ GroupMap group_map(const GroupedParams& p, int lane) {
@@ -101,15 +149,25 @@ __device__ __forceinline__ void group_split(const GroupedParams& p, StepCursor& 
   }
 }
 
+constexpr int kNoUnit = -(1 << 30);  // past the stream's end, and so is the unit after it
+
 // Unit u of the stream: the units of one group are consecutive, rastered in
 // bands of group_m tile rows, and the XCD remap gives each XCD consecutive
 // units, so that a group's weight is read into one XCD's L2.
 template <int BM, int BN, bool ROWS>
 __device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const GroupMap& m, int unit) {
   StepCursor c;
-  c.u = unit;
   c.kt = c.kt0 = c.split = 0;
-  int id = __builtin_amdgcn_readfirstlane(xcd_remap(min(unit, m.total - 1), m.total));
+  int id;
+  if constexpr (ROWS) {
+    c.u = unit < m.total ? unit : kNoUnit;
+    id = __builtin_amdgcn_readfirstlane(xcd_remap(min(unit, m.total - 1), m.total));
+  } else {
+    const int round = unit / (int)gridDim.x;
+    id = round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - m.place : m.place);
+    c.u = unit >= 0 && id < m.total ? unit : kNoUnit;
+    id = __builtin_amdgcn_readfirstlane(min(max(id, 0), m.total - 1));
+  }
   if (p.splits > 1) {
     const int per_split = m.total / p.splits;
     c.split = id / per_split;
@@ -142,6 +200,7 @@ __device__ __forceinline__ StepCursor group_cursor(const GroupedParams& p, const
   } else {
     c.b = id / (p.tiles_m * p.tiles_n);
     t = id - c.b * (p.tiles_m * p.tiles_n);
+    if (p.ordered) c.b = (__builtin_amdgcn_readlane(m.order, c.b >> 2) >> (8 * (c.b & 3))) & 255;
     int end;
     group_rows(p.offsets, p.rows, c.b, c.base, end);
     c.count = end - c.base;
