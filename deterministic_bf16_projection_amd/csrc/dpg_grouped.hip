@@ -163,7 +163,7 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   if (empty) return DPG_OK;
   if (E > 0 && (!offsets || ((uintptr_t)offsets & 3u))) return offsets ? DPG_ERR_ALIGNMENT : DPG_ERR_INVALID_ARG;
   // a tile is addressed through 32-bit buffer offsets, rows and units through 32-bit indexes
-  if (std::max(lda, ldb) >= (1 << 22)) return DPG_ERR_UNSUPPORTED;
+  if (std::max(lda, ldb) >= (1 << 22) || (mc.rows > 1 && ldc >= (1 << 21))) return DPG_ERR_UNSUPPORTED;
   if (R >= (1ll << 31) - 512 || N >= (1ll << 31) - 512 || K >= (1ll << 31) - 512 || E >= (1ll << 24))
     return DPG_ERR_UNSUPPORTED;
 
@@ -173,7 +173,7 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   p.c = c;
   p.lda = lda;
   p.ldb = ldb;
-  p.ldc = ldc;
+  p.ldc = mc.rows > 1 ? ldc : mc.cols;  // of one row the stride is never used, whatever it is
   p.M = (int)(wgrad ? N : R);
   p.N = (int)(layout == LAYOUT_FWD ? N : K);
   p.K = (int)(layout == LAYOUT_FWD ? K : N);  // weight gradient: each group's rows

@@ -523,6 +523,12 @@ struct FastGemm {
   // groups (GR_ROWS), the weight gradient the reduction (one output per group)
   static constexpr bool GR_ROWS = GR && A_KMAJ;
   static_assert(!GR || (!X3 && !SK), "grouped products: BF16, whole reductions");
+  // Output through store_bounded: 1.6% faster for the forward and the input
+  // gradient (65536 skewed rows of 64 groups, 1024 x 4096: 558 -> 549 and 593
+  // -> 584 us), 8% for the four-wave weight gradient (2001 rows, 16 groups, 512
+  // x 1024: 13.8 -> 12.7); the eight-wave weight gradient is 2% faster without
+  // (630 and 642 us).
+  static constexpr bool GR_BOUNDED = GR && (GR_ROWS || ROLE == ROLE_BOTH);
   typedef typename std::conditional<X3, FastOperandX3<BM, A_KMAJ, NTL>, FastOperand<BM, A_KMAJ, NTL>>::type OpA;
   typedef typename std::conditional<X3, FastOperandX3<BN, B_KMAJ, NTL>, FastOperand<BN, B_KMAJ, NTL>>::type OpB;
   // Who stages what.  A K-major A (X in the forward pass, dY in the input
@@ -578,9 +584,10 @@ struct FastGemm {
   static __device__ __forceinline__ void epilogue(const Params& p, const StepCursor& c, int lane, int wm, int wn,
                                                   f32x16 (&acc)[FM][FN], char* scr) {
     char* out;
-    if constexpr (GR_ROWS) {
-      out = (char*)p.c + ((int64_t)c.base * p.ldc + (int64_t)c.split * p.split_stride) * (OUT == OUT_BF16 ? 2 : 4);
-      store_tile<OUT>(out, p.ldc, 0, 0, c.count, p.N, c.row0, c.col0, lane, wm, wn, acc, scr);
+    if constexpr (GR_BOUNDED) {
+      const int64_t first = GR_ROWS ? (int64_t)c.base * p.ldc : (int64_t)c.b * p.batch_c;
+      store_bounded<OUT>((char*)p.c + (first + (int64_t)c.split * p.split_stride) * (OUT == OUT_BF16 ? 2 : 4), p.ldc,
+                         GR_ROWS ? c.count : p.M, p.N, c.row0, c.col0, lane, wm, wn, acc, scr);
       return;
     }
     if (OUT == OUT_PARTIAL || (GR && OUT == OUT_F32))
@@ -649,6 +656,73 @@ struct FastGemm {
             const f32x4 v = *(const f32x4*)(scr + r * 128 + ((cc ^ rr ^ k) << 4));
             const int m = m0 + r, n = col0 + wn * WN + j * 32 + cc * 4;
             if (m < M && n < N) *(f32x4*)(out + ((int64_t)(m - mo) * ldc + (n - no)) * 4) = v;
+          }
+        }
+      }
+    }
+  }
+
+  // The same through buffer stores, whose descriptor ends with the tile's valid
+  // rows, and whose offset is put past it in columns beyond N: no branches and
+  // no 64-bit addresses, so that a block's stores go out while the next one
+  // passes the LDS buffer.  The rows of a tile span less than 2^31 bytes.
+  template <int EOUT>
+  static __device__ __forceinline__ void store_bounded(char* out, int64_t ldc, int M, int N, int row0, int col0,
+                                                       int lane, int wm, int wn, f32x16 (&acc)[FM][FN], char* scr) {
+    static_assert(FN == 2, "a wave's row segment is 64 columns");
+    constexpr int ELT = EOUT == OUT_BF16 ? 2 : 4;
+    constexpr int kStreaming = 2;  // the tile is not read again here
+    asm volatile("" : "+v"(lane));
+    const int lr = lane & 31, lh = lane >> 5;
+    const int sw = fswz(lr);
+    const int rr = lane >> 3, cc = lane & 7;
+    const int ld = (int)ldc;
+    const int rows = min(M - row0, BM);
+    const rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(out + ((int64_t)row0 * ldc + col0) * ELT, (short)0,
+                                                        max(((rows - 1) * ld + (N - col0)) * ELT, 0), 0x00020000);
+    constexpr int CHUNK = 16 / ELT;  // elements of a lane's store
+    constexpr int HALVES = EOUT == OUT_BF16 ? 1 : 2;
+    uint32_t voff[HALVES];
+#pragma unroll
+    for (int j = 0; j < HALVES; ++j) {
+      const int n = wn * WN + j * 32 + cc * CHUNK;
+      voff[j] = (uint32_t)(((row_start(wm) + rr) * ld + n) * ELT) | (col0 + n < N ? 0u : 0x80000000u);
+    }
+    const uint32_t step = (uint32_t)(8 * ld * ELT);  // eight rows on
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (EOUT == OUT_BF16) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // chunks as in store_tile
+            const int q0 = 2 * h, q1 = 2 * h + 1;
+            const uint32_t x0 = pack_bf16x2(acc[i][j][4 * q0], acc[i][j][4 * q0 + 1]);
+            const uint32_t x1 = pack_bf16x2(acc[i][j][4 * q0 + 2], acc[i][j][4 * q0 + 3]);
+            const uint32_t y0 = pack_bf16x2(acc[i][j][4 * q1], acc[i][j][4 * q1 + 1]);
+            const uint32_t y1 = pack_bf16x2(acc[i][j][4 * q1 + 2], acc[i][j][4 * q1 + 3]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+            const int chunk = 4 * j + 2 * h + lh;
+            *(u32x4*)(scr + lr * 128 + ((chunk ^ sw) << 4)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u32x4 v = *(const u32x4*)(scr + (8 * k + rr) * 128 + ((cc ^ rr ^ k) << 4));
+          __builtin_amdgcn_raw_buffer_store_b128(v, rs, (int)(voff[0] + (uint32_t)(4 * i + k) * step), 0, kStreaming);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *(f32x4*)(scr + lr * 128 + (((2 * q + lh) ^ sw) << 4)) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const u32x4 v = *(const u32x4*)(scr + (8 * k + rr) * 128 + ((cc ^ rr ^ k) << 4));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rs, (int)(voff[j] + (uint32_t)(4 * i + k) * step), 0, kStreaming);
           }
         }
       }
