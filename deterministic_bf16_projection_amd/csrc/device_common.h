@@ -128,4 +128,52 @@ __device__ __forceinline__ float wave_sum(float v) {
   return lane_f32(v, 63);
 }
 
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// of each half of the wave, in its last lane
+__device__ __forceinline__ int half_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+}
+
+// The same within rows of 16 lanes, by rotations: every lane holds the result
+// (the same bits: each step adds the same two sums on both lanes of a pair).
+template <int N>
+__device__ __forceinline__ float row_rotate(float v) {
+  return dpp_f32<0x120 | N, 0xf>(v, v);
+}
+template <int N>
+__device__ __forceinline__ unsigned row_rotate(unsigned v) {
+  return (unsigned)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 | N, 0xf, 0xf, false);
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, row_rotate<8>(v));
+  v = fmaxf(v, row_rotate<4>(v));
+  v = fmaxf(v, row_rotate<2>(v));
+  return fmaxf(v, row_rotate<1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += row_rotate<8>(v);
+  v += row_rotate<4>(v);
+  v += row_rotate<2>(v);
+  return v + row_rotate<1>(v);
+}
+__device__ __forceinline__ unsigned row_min(unsigned v) {
+  v = min(v, row_rotate<8>(v));
+  v = min(v, row_rotate<4>(v));
+  v = min(v, row_rotate<2>(v));
+  return min(v, row_rotate<1>(v));
+}
+
 }  // namespace dpg

@@ -10,32 +10,35 @@
 namespace dpg {
 namespace {
 
-// Tokens of one block of the choice: 64 (four per wave), more where the
-// counts of the blocks would pass 512 rows; all of them in one block up to 64.
-constexpr int kTokensPerBlock = 64, kMaxBlocks = 512;
+// Tokens of one block of the choice: 64, one round of its waves, more where
+// there would be over 512 blocks.  Up to 64 tokens are one block.
+constexpr int kMaxBlocks = 512;
+// a block's counts are kept in 16 bits
+constexpr int64_t kMaxTokens = (int64_t)kMaxBlocks * (65535 / kRouteRound) * kRouteRound;
 
 struct RouteGrid {
   int tokens_per_block, blocks;
+  int hist_ld() const { return (blocks + 7) & ~7; }  // rows of 16 bytes
 };
 
 RouteGrid route_grid(int64_t T) {
   RouteGrid g;
-  g.tokens_per_block = kTokensPerBlock;
-  if (T > (int64_t)kTokensPerBlock * kMaxBlocks)
-    g.tokens_per_block = (int)((T + kMaxBlocks * kRouteWaves - 1) / (kMaxBlocks * kRouteWaves)) * kRouteWaves;
+  const int64_t per_round = (int64_t)kMaxBlocks * kRouteRound;
+  g.tokens_per_block = (int)(std::max<int64_t>(1, (T + per_round - 1) / per_round) * kRouteRound);
   g.blocks = (int)((T + g.tokens_per_block - 1) / g.tokens_per_block);
   return g;
 }
 
 dpg_status check_route(int64_t T, int64_t E, int64_t top_k) {
   if (T < 0 || E < 1 || top_k < 1 || top_k > E) return DPG_ERR_INVALID_ARG;
-  if (E > kRouteMaxExperts || top_k > kRouteMaxTopK || T > ((1ll << 31) - 1) / top_k) return DPG_ERR_UNSUPPORTED;
+  if (E > kRouteMaxExperts || top_k > kRouteMaxTopK || T > ((1ll << 31) - 1) / top_k || T > kMaxTokens)
+    return DPG_ERR_UNSUPPORTED;
   return DPG_OK;
 }
 
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
-// registers of logits per lane: 64, 128, 256 or 512 experts
+// registers of logits per lane of 16 (choice) or 64 (gradient): 64, 128, 256 or 512 experts
 int expert_regs(int64_t E) { return E <= 64 ? 0 : E <= 128 ? 1 : E <= 256 ? 2 : 3; }
 
 typedef void (*ChooseFn)(RouteParams);
@@ -50,6 +53,16 @@ int row_lanes_log2(int64_t chunks) {
   while (n < 8 && (1 << n) < chunks) ++n;
   return n;
 }
+
+// Workgroups for n tokens or slots, `each` of them to one: a launch takes fewer
+// than 2^32 threads, so the kernels go round beyond 2^22 workgroups.
+int64_t row_grid(int64_t n, int64_t each) { return std::min<int64_t>((n + each - 1) / each, 1 << 22); }
+
+// Sorted rows that do not fit the XCDs' 32 MB of L2 go past it, which leaves
+// it to the token side: routing of 16384 tokens, 8 slots of 4096 columns, forward
+// and backward, 1247 us without and 1174 with.  Smaller ones stay for the
+// product that reads them next.
+bool stream_rows(int64_t R, int64_t H, int elt) { return R * H >= (int64_t)(32 << 20) / elt; }
 
 dpg_status check_rows(const void* positions, const void* offsets, int64_t T, int64_t R, int64_t H, int64_t E,
                       int64_t top_k) {
@@ -74,7 +87,7 @@ extern "C" {
 size_t dpg_route_workspace_size(int64_t T, int64_t E, int64_t top_k) {
   if (check_route(T, E, top_k) != DPG_OK) return (size_t)-1;
   const RouteGrid g = route_grid(T);
-  return g.blocks > 1 ? (size_t)g.blocks * (size_t)(E + 1) * sizeof(int32_t) : 0;
+  return g.blocks > 1 ? (size_t)g.hist_ld() * (size_t)E * sizeof(uint16_t) : 0;
 }
 
 dpg_status dpg_route(const float* logits, int64_t ldl, int64_t T, int64_t E, int64_t top_k, int renormalize,
@@ -89,7 +102,7 @@ dpg_status dpg_route(const float* logits, int64_t ldl, int64_t T, int64_t E, int
     return DPG_ERR_ALIGNMENT;
   const RouteGrid g = route_grid(T);
   const size_t need = dpg_route_workspace_size(T, E, top_k);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned4(workspace))) return DPG_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DPG_ERR_WORKSPACE;
 
   RouteParams p{};
   p.logits = logits;
@@ -105,20 +118,26 @@ dpg_status dpg_route(const float* logits, int64_t ldl, int64_t T, int64_t E, int
   p.offsets = offsets;
   p.rows = rows;
   p.positions = positions;
-  p.hist = (int32_t*)workspace;
-  static const ChooseFn choose_one[4] = {&route_choose_kernel<1, true>, &route_choose_kernel<2, true>,
-                                         &route_choose_kernel<4, true>, &route_choose_kernel<8, true>};
-  static const ChooseFn choose_many[4] = {&route_choose_kernel<1, false>, &route_choose_kernel<2, false>,
-                                          &route_choose_kernel<4, false>, &route_choose_kernel<8, false>};
+  p.hist_ld = g.hist_ld();
+  p.hist = (uint16_t*)workspace;
+  // one wave a token up to 16 tokens, rows of 16 lanes beyond
+  static const ChooseFn wide[4] = {&route_choose_kernel<64, 1, true>, &route_choose_kernel<64, 2, true>,
+                                   &route_choose_kernel<64, 4, true>, &route_choose_kernel<64, 8, true>};
+  static const ChooseFn one[4] = {&route_choose_kernel<16, 4, true>, &route_choose_kernel<16, 8, true>,
+                                  &route_choose_kernel<16, 16, true>, &route_choose_kernel<16, 32, true>};
+  static const ChooseFn many[4] = {&route_choose_kernel<16, 4, false>, &route_choose_kernel<16, 8, false>,
+                                   &route_choose_kernel<16, 16, false>, &route_choose_kernel<16, 32, false>};
   const int keys = p.E + 1;
   void* args[] = {&p};
-  if (g.blocks <= 1)  // T = 0 too: the offsets become zeros
-    return launch((const void*)choose_one[expert_regs(E)], 1, kRouteThreads,
-                  (size_t)(2 + kRouteWaves) * keys * sizeof(int), args, stream);
-  st = launch((const void*)choose_many[expert_regs(E)], g.blocks, kRouteThreads, keys * sizeof(int), args, stream);
+  if (g.blocks <= 1) {  // T = 0 too: the offsets become zeros
+    const int threads = T <= 4 ? 256 : kRouteThreads;
+    return launch((const void*)(T <= 16 ? wide : one)[expert_regs(E)], 1, threads,
+                  (size_t)((2 + threads / 64) * keys + T * top_k) * sizeof(int), args, stream);
+  }
+  st = launch((const void*)many[expert_regs(E)], g.blocks, kRouteThreads, keys * sizeof(int), args, stream);
   if (st != DPG_OK) return st;
   return launch((const void*)&route_order_kernel, g.blocks, kRouteThreads,
-                (size_t)(3 + kRouteWaves) * keys * sizeof(int), args, stream);
+                (size_t)(3 + kRouteThreads / 64) * keys * sizeof(int), args, stream);
 }
 
 dpg_status dpg_route_dgrad(const float* logits, int64_t ldl, const int32_t* experts, const float* weights,
@@ -134,7 +153,7 @@ dpg_status dpg_route_dgrad(const float* logits, int64_t ldl, const int32_t* expe
                                      &route_dgrad_kernel<8>};
   int e = (int)E, k = (int)top_k, renorm = renormalize != 0;
   void* args[] = {&logits, &ldl, &experts, &weights, &dweights, &dlogits, &lddl, &T, &e, &k, &renorm};
-  return launch((const void*)fns[expert_regs(E)], (T + 3) / 4, 256, 0, args, stream);
+  return launch((const void*)fns[expert_regs(E)], row_grid(T, 4), 256, 0, args, stream);
 }
 
 dpg_status dpg_dispatch(const void* x, int64_t ldx, const int32_t* positions, const int32_t* offsets, void* xs,
@@ -160,8 +179,10 @@ dpg_status dpg_dispatch(const void* x, int64_t ldx, const int32_t* positions, co
   p.k = (int)top_k;
   p.lanes_log2 = row_lanes_log2(H * elt / 16);
   void* args[] = {&p};
-  const RowsFn fn = elt == 2 ? &dispatch_kernel<2> : &dispatch_kernel<4>;
-  return launch((const void*)fn, ((T << p.lanes_log2) + 255) / 256, 256, 0, args, stream);
+  const bool past = stream_rows(R, H, elt);
+  const RowsFn fn = elt == 2 ? (past ? &dispatch_kernel<2, true> : &dispatch_kernel<2, false>)
+                             : (past ? &dispatch_kernel<4, true> : &dispatch_kernel<4, false>);
+  return launch((const void*)fn, row_grid(T, 256 >> p.lanes_log2), 256, 0, args, stream);
 }
 
 dpg_status dpg_combine(const void* ys, int64_t ldys, dpg_dtype ys_dtype, const int32_t* positions,
@@ -188,10 +209,13 @@ dpg_status dpg_combine(const void* ys, int64_t ldys, dpg_dtype ys_dtype, const i
   p.k = (int)top_k;
   p.lanes_log2 = row_lanes_log2(H / 8);
   void* args[] = {&p};
-  const bool in4 = ys_dtype == DPG_F32, out4 = y_dtype == DPG_F32;
-  const RowsFn fn = in4 ? (out4 ? &combine_kernel<4, 4> : &combine_kernel<4, 2>)
-                        : (out4 ? &combine_kernel<2, 4> : &combine_kernel<2, 2>);
-  return launch((const void*)fn, ((T << p.lanes_log2) + 255) / 256, 256, 0, args, stream);
+  static const RowsFn fns[2][2][2] = {
+      {{&combine_kernel<2, 2, false>, &combine_kernel<2, 2, true>},
+       {&combine_kernel<2, 4, false>, &combine_kernel<2, 4, true>}},
+      {{&combine_kernel<4, 2, false>, &combine_kernel<4, 2, true>},
+       {&combine_kernel<4, 4, false>, &combine_kernel<4, 4, true>}}};
+  const RowsFn fn = fns[ys_dtype == DPG_F32][y_dtype == DPG_F32][stream_rows(R, H, elt_size((int)ys_dtype))];
+  return launch((const void*)fn, row_grid(T, 256 >> p.lanes_log2), 256, 0, args, stream);
 }
 
 dpg_status dpg_combine_dgrad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* positions,
@@ -224,8 +248,10 @@ dpg_status dpg_combine_dgrad(const void* dy, int64_t lddy, const void* ys, int64
   p.H = (int)H;
   p.k = (int)top_k;
   void* args[] = {&p};
-  const RowsFn fn = elt == 2 ? &combine_dgrad_kernel<2> : &combine_dgrad_kernel<4>;
-  return launch((const void*)fn, (T + 3) / 4, 256, 0, args, stream);
+  const bool past = stream_rows(R, H, elt);
+  const RowsFn fn = elt == 2 ? (past ? &combine_dgrad_kernel<2, true> : &combine_dgrad_kernel<2, false>)
+                             : (past ? &combine_dgrad_kernel<4, true> : &combine_dgrad_kernel<4, false>);
+  return launch((const void*)fn, row_grid(T * top_k, 4), 256, 0, args, stream);
 }
 
 }  // extern "C"

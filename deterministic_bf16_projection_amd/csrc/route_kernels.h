@@ -7,9 +7,9 @@
 namespace dpg {
 
 constexpr int kRouteThreads = 1024;
-constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteMaxExperts = 512;
 constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteRound = 64;          // tokens of a block that are chosen for at once
 
 // -------------------------------------------------------------- choice --
 struct RouteParams {
@@ -17,73 +17,93 @@ struct RouteParams {
   int64_t ldl;
   int64_t T;
   int E, k, renorm;
-  int tokens_per_block;  // blocks of consecutive tokens
-  int blocks;
+  int tokens_per_block;  // blocks of consecutive tokens, a multiple of kRouteRound
+  int blocks, hist_ld;
   int32_t* experts;      // [T, k]
   float* weights;        // [T, k]
   int32_t* offsets;      // [E + 1]
   int32_t* rows;         // [T k]
   int32_t* positions;    // [T, k]
-  int32_t* hist;         // [blocks, E + 1]
+  uint16_t* hist;        // [E, hist_ld]: counts of the blocks
 };
 
-// One token by one wave.  The logits sit in registers, lane l holding experts
-// l, 64 + l, ...; each of the k rounds takes the maximum over the wave and,
-// among equal ones, the lowest expert (registers in ascending order, then the
-// lowest lane of a ballot).  Only a logit of -infinity masks an expert; a NaN
-// is never chosen but makes the token's weights NaN.  Lane j returns choice j.
-template <int NR>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& expert, float& weight) {
+// One token by LANES lanes: a row of 16, four tokens to a wave, or the whole
+// wave.  The logits sit in registers, lane l holding the experts l, LANES + l,
+// ...; each of the k rounds takes the maximum over the lanes and, among equal
+// ones, the lowest expert.  Only a logit of -infinity masks an expert; a NaN is
+// never chosen but makes the token's weights NaN.  Lane l returns the choices
+// l and (rows of 16) 16 + l.
+//
+// Many tokens are bound by the rounds' instructions, of which four tokens in a
+// wave share most (16384 tokens of 256 experts, 8 chosen: 20 us with a token
+// to a wave, 11 with rows).  A few tokens wait for their dependent steps,
+// which are fewer with 64 lanes (one token: 6.1 us, 7.5 with a row).
+template <int LANES, int NR>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, bool live, int lane, int (&expert)[2],
+                                       float (&weight)[2]) {
+  constexpr bool ROW = LANES == 16;
+  static_assert(ROW || LANES == 64, "a row or a wave");
+  const auto lanes_max = [](float x) { return ROW ? row_max(x) : wave_max(x); };
+  const auto lanes_sum = [](float x) { return ROW ? row_sum(x) : wave_sum(x); };
   const float kMasked = -__builtin_inff();
+  const int sub = lane & (LANES - 1);
   float v[NR];
   bool nan = false;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    const int i = r * 64 + lane;
-    const float x = i < p.E ? p.logits[t * p.ldl + i] : kMasked;
+    const int i = r * LANES + sub;
+    const float x = live && i < p.E ? p.logits[t * p.ldl + i] : kMasked;
     nan |= x != x;
     v[r] = x != x ? kMasked : x;
   }
-  const bool any_nan = __ballot(nan) != 0;
+  const uint64_t nans = __ballot(nan);
+  const bool any_nan = ROW ? ((nans >> (lane & 48)) & 0xffff) != 0 : nans != 0;
   float local = v[0];
 #pragma unroll
   for (int r = 1; r < NR; ++r) local = fmaxf(local, v[r]);
-  const float top = wave_max(local);
+  const float top = lanes_max(local);
   float total = 0.f;
-  if (!p.renorm && top > kMasked) {
+  if (!p.renorm) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) total += expf(v[r] - top);
-    total = wave_sum(total);
+    for (int r = 0; r < NR; ++r) total += top > kMasked ? expf(v[r] - top) : 0.f;
+    total = lanes_sum(total);
   }
-  expert = -1;
-  float mine = kMasked;
+  float mine[2] = {kMasked, kMasked};
+  expert[0] = expert[1] = -1;
   float m = top;
-  for (int j = 0; j < p.k && m > kMasked; ++j) {
-    int at = 0;
-    bool found = false;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const uint64_t eq = __ballot(v[r] == m);
-      if (!found && eq) {
-        const int l = __builtin_ctzll(eq);
-        at = r * 64 + l;
-        if (lane == l) v[r] = kMasked;
-        found = true;
+  for (int half = 0; half < (ROW ? 2 : 1); ++half) {
+    for (int j = LANES * half; j < min(p.k, LANES * half + LANES); ++j) {
+      if (__ballot(m > kMasked) == 0) break;  // all the wave's tokens are out of experts
+      unsigned at = 0xffffu;
+      if constexpr (ROW) {
+#pragma unroll
+        for (int r = NR - 1; r >= 0; --r) at = v[r] == m ? (unsigned)(r * 16 + sub) : at;
+        at = row_min(at);
+      } else {
+#pragma unroll
+        for (int r = NR - 1; r >= 0; --r) {
+          const uint64_t eq = __ballot(v[r] == m);
+          if (eq) at = (unsigned)(r * 64 + __builtin_ctzll(eq));
+        }
       }
-    }
-    if (lane == j) {
-      expert = at;
-      mine = m;
-    }
-    local = v[0];
+      if (sub == (j & (LANES - 1)) && m > kMasked) {
+        expert[half] = (int)at;
+        mine[half] = m;
+      }
+      const unsigned d = at - (unsigned)sub;
 #pragma unroll
-    for (int r = 1; r < NR; ++r) local = fmaxf(local, v[r]);
-    m = wave_max(local);
+      for (int r = 0; r < NR; ++r) v[r] = d == (unsigned)(r * LANES) ? kMasked : v[r];
+      local = v[0];
+#pragma unroll
+      for (int r = 1; r < NR; ++r) local = fmaxf(local, v[r]);
+      m = lanes_max(local);
+    }
   }
-  const float e = expert >= 0 ? expf(mine - top) : 0.f;
-  if (p.renorm) total = wave_sum(e);
-  weight = expert >= 0 ? e / total : 0.f;
-  if (any_nan && expert >= 0) weight = __builtin_nanf("");
+  const float e0 = expert[0] >= 0 ? expf(mine[0] - top) : 0.f, e1 = expert[1] >= 0 ? expf(mine[1] - top) : 0.f;
+  if (p.renorm) total = lanes_sum(e0 + e1);
+  weight[0] = expert[0] < 0 ? 0.f : any_nan ? __builtin_nanf("") : e0 / total;
+  weight[1] = expert[1] < 0 ? 0.f : any_nan ? __builtin_nanf("") : e1 / total;
 }
 
 // --------------------------------------------------------- stable order --
@@ -93,23 +113,25 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
 // slots; the counts per (wave, expert) in LDS, summed over the waves before,
 // give every wave its own running places, and inside a wave the lanes with
 // equal experts are found with one ballot per bit.  Integer counts: no order
-// matters, the result is the same every time.
-__device__ __forceinline__ void scatter_block(const RouteParams& p, int64_t slot0, int slots, const int* start,
-                                              int* counts /* waves x (E + 1) */, int tid) {
+// matters, the result is the same every time.  `experts` are the block's
+// (unused: negative), in LDS or in memory.
+__device__ __forceinline__ void scatter_block(const RouteParams& p, int64_t slot0, int slots, const int* experts,
+                                              const int* start, int* counts /* waves x (E + 1) */, int tid) {
   const int keys = p.E + 1;
+  const int threads = blockDim.x, waves = threads >> 6;
   const int lane = tid & 63, wave = tid >> 6;
-  const int per_wave = ((slots + kRouteWaves - 1) / kRouteWaves + 63) & ~63;
+  const int per_wave = ((slots + waves - 1) / waves + 63) & ~63;
   const int s0 = wave * per_wave, s1 = min(slots, s0 + per_wave);
-  for (int i = tid; i < kRouteWaves * keys; i += kRouteThreads) counts[i] = 0;
+  for (int i = tid; i < waves * keys; i += threads) counts[i] = 0;
   __syncthreads();
   for (int s = s0 + lane; s < s1; s += 64) {
-    const int e = p.experts[slot0 + s];
+    const int e = experts[s];
     atomicAdd(&counts[wave * keys + (e < 0 ? p.E : e)], 1);
   }
   __syncthreads();
-  for (int key = tid; key < keys; key += kRouteThreads) {
+  for (int key = tid; key < keys; key += threads) {
     int at = start[key];
-    for (int w = 0; w < kRouteWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
       const int n = counts[w * keys + key];
       counts[w * keys + key] = at;
       at += n;
@@ -122,7 +144,7 @@ __device__ __forceinline__ void scatter_block(const RouteParams& p, int64_t slot
     const bool live = s < s1;
     int key = p.E;
     if (live) {
-      const int e = p.experts[slot0 + s];
+      const int e = experts[s];
       key = e < 0 ? p.E : e;
     }
     uint64_t same = __ballot(live);
@@ -169,42 +191,79 @@ __device__ __forceinline__ void prefix_experts(const int* total, int* first, int
   }
 }
 
-// Choice of the block's tokens and its counts per expert.  With ONE (all
-// tokens in one block) the order follows in the same launch.
-template <int NR, bool ONE>
+// The order of at most 64 slots: each thread counts the slots before its own,
+// and before its expert's first.
+__device__ __forceinline__ void order_few(const RouteParams& p, int slots, const int* experts, int tid) {
+  if (tid < slots) {
+    const int key = experts[tid];
+    int at = 0;
+    for (int i = 0; i < slots; ++i) at += experts[i] < key || (experts[i] == key && i < tid);
+    p.rows[at] = tid;
+    p.positions[tid] = at;
+  }
+  for (int key = tid; key <= p.E; key += blockDim.x) {
+    int at = 0;
+    for (int i = 0; i < slots; ++i) at += experts[i] < key;
+    p.offsets[key] = at;
+  }
+}
+
+// Choice of the block's tokens (threads / LANES at a time) and its counts per
+// expert.  With ONE (all tokens in one block, at most kRouteRound) the order
+// follows in the same launch.  LDS: counts; with ONE also their prefix, the
+// counts per wave and the slots' experts.
+template <int LANES, int NR, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(RouteParams p) {
   extern __shared__ int lds[];
   const int keys = p.E + 1;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   int* total = lds;
-  for (int i = tid; i < keys; i += kRouteThreads) total[i] = 0;
-  __syncthreads();
+  int* slot_experts = lds + (2 + (threads >> 6)) * keys;  // ONE: unused slots as expert E
+  const int64_t slots = p.T * p.k;
+  const bool few = ONE && slots <= 64;  // ordered without counts
+  if (!few) {
+    for (int i = tid; i < keys; i += threads) total[i] = 0;
+    __syncthreads();
+  }
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_block;
   const int64_t t1 = min(p.T, t0 + p.tokens_per_block);
-  for (int64_t t = t0 + wave; t < t1; t += kRouteWaves) {
-    int expert;
-    float weight;
-    choose<NR>(p, t, lane, expert, weight);
-    if (lane < p.k) {
-      p.experts[t * p.k + lane] = expert;
-      p.weights[t * p.k + lane] = weight;
-      atomicAdd(&total[expert < 0 ? p.E : expert], 1);
+  for (int64_t first = t0; first < t1; first += threads / LANES) {
+    const int64_t t = first + tid / LANES;
+    const bool live = t < t1;
+    if (__ballot(live) == 0) continue;
+    int expert[2];
+    float weight[2];
+    choose<LANES, NR>(p, t, live, lane, expert, weight);
+#pragma unroll
+    for (int half = 0; half < (LANES == 16 ? 2 : 1); ++half) {
+      const int j = LANES * half + (lane & (LANES - 1));
+      if (live && j < p.k) {
+        const int key = expert[half] < 0 ? p.E : expert[half];
+        p.experts[t * p.k + j] = expert[half];
+        p.weights[t * p.k + j] = weight[half];
+        if (!few) atomicAdd(&total[key], 1);
+        if (ONE) slot_experts[t * p.k + j] = key;
+      }
     }
   }
   __syncthreads();
-  if (ONE) {
+  if (few) {
+    order_few(p, (int)slots, slot_experts, tid);
+  } else if (ONE) {
     int* first = lds + keys;
-    if (wave == 0) prefix_experts(total, first, keys, lane);
+    if (tid < 64) prefix_experts(total, first, keys, lane);
     __syncthreads();
-    for (int i = tid; i < keys; i += kRouteThreads) p.offsets[i] = first[i];
-    scatter_block(p, 0, (int)(p.T * p.k), first, lds + 2 * keys, tid);
+    for (int i = tid; i < keys; i += threads) p.offsets[i] = first[i];
+    scatter_block(p, 0, (int)slots, slot_experts, first, lds + 2 * keys, tid);
   } else {
-    for (int i = tid; i < keys; i += kRouteThreads) p.hist[(int64_t)blockIdx.x * keys + i] = total[i];
+    for (int i = tid; i < p.E; i += threads) p.hist[(int64_t)i * p.hist_ld + blockIdx.x] = (uint16_t)total[i];
   }
 }
 
 // The order, from the counts of all blocks: each block sums the counts of the
-// blocks before it and of all, so that no launch lies between.
+// blocks before it and of all, so that no launch lies between.  32 lanes read
+// 256 blocks' counts of one expert; a wave has eight such pairs in flight.
 __global__ void __launch_bounds__(kRouteThreads) route_order_kernel(RouteParams p) {
   extern __shared__ int lds[];
   const int keys = p.E + 1;
@@ -212,34 +271,59 @@ __global__ void __launch_bounds__(kRouteThreads) route_order_kernel(RouteParams 
   int* total = lds;
   int* before = lds + keys;
   int* first = lds + 2 * keys;
-  for (int i = tid; i < 2 * keys; i += kRouteThreads) lds[i] = 0;
-  __syncthreads();
-  // a part of the threads' groups takes every blocks / groups-th block
-  const int width = (keys + 63) & ~63;
-  const int groups = kRouteThreads / width;
-  const int g = tid / width, key = tid - g * width;
-  if (g < groups && key < keys) {
-    int all = 0, prev = 0;
-#pragma unroll 8
-    for (int b = g; b < p.blocks; b += groups) {
-      const int n = p.hist[(int64_t)b * keys + key];
-      all += n;
-      prev += b < (int)blockIdx.x ? n : 0;
+  const int64_t slot0 = (int64_t)blockIdx.x * p.tokens_per_block * p.k;
+  const int64_t slots = p.T * p.k;
+  constexpr int G = 8;
+  for (int key0 = wave * 2 * G; key0 < p.E; key0 += kRouteThreads / 64 * 2 * G) {
+    int all[G], prev[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) all[g] = prev[g] = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += 256) {
+      const int b = b0 + (lane & 31) * 8;
+      u32x4 n[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        n[g] = b < p.hist_ld
+                   ? *(const u32x4*)(p.hist + (int64_t)min(key0 + 2 * g + (lane >> 5), p.E - 1) * p.hist_ld + b)
+                   : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (int)((n[g][i >> 1] >> (16 * (i & 1))) & 0xffffu);
+          all[g] += b + i < p.blocks ? c : 0;
+          prev[g] += b + i < (int)blockIdx.x ? c : 0;
+        }
     }
-    atomicAdd(&total[key], all);
-    atomicAdd(&before[key], prev);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      all[g] = half_sum(all[g]);
+      prev[g] = half_sum(prev[g]);
+      const int key = key0 + 2 * g + (lane >> 5);
+      if ((lane & 31) == 31 && key < p.E) {
+        total[key] = all[g];
+        before[key] = prev[g];
+      }
+    }
   }
+  if (tid == 0) total[p.E] = 0;  // the last prefix needs none
   __syncthreads();
   if (wave == 0) prefix_experts(total, first, keys, lane);
+  // the unused slots of the blocks before: what their experts did not take
+  if (wave == 1) {
+    int used = 0;
+    for (int i = lane; i < p.E; i += 64) used += before[i];
+    used = wave_sum(used);
+    if (lane == 0) before[p.E] = (int)(slot0 - used);
+  }
   __syncthreads();
   for (int i = tid; i < keys; i += kRouteThreads) {
     if (blockIdx.x == 0) p.offsets[i] = first[i];
     first[i] += before[i];
   }
   __syncthreads();
-  const int64_t slot0 = (int64_t)blockIdx.x * p.tokens_per_block * p.k;
-  const int64_t left = p.T * p.k - slot0;
-  scatter_block(p, slot0, (int)min(left, (int64_t)p.tokens_per_block * p.k), first, lds + 3 * keys, tid);
+  scatter_block(p, slot0, (int)min(slots - slot0, (int64_t)p.tokens_per_block * p.k), p.experts + slot0, first,
+                lds + 3 * keys, tid);
 }
 
 // Gradient of the weights by the logits, one wave per token.  With q the
@@ -251,55 +335,55 @@ __global__ void __launch_bounds__(256) route_dgrad_kernel(const float* logits, i
                                                           const float* weights, const float* dweights, float* dlogits,
                                                           int64_t ldd, int64_t T, int E, int k, int renorm) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;
-  int e = -1;
-  float w = 0.f, d = 0.f;
-  if (lane < k) {
-    e = experts[t * k + lane];
-    if (e >= 0) {
-      w = weights[t * k + lane];
-      d = w * dweights[t * k + lane];
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += (int64_t)gridDim.x * 4) {
+    int e = -1;
+    float w = 0.f, d = 0.f;
+    if (lane < k) {
+      e = experts[t * k + lane];
+      if (e >= 0) {
+        w = weights[t * k + lane];
+        d = w * dweights[t * k + lane];
+      }
     }
-  }
-  const float inner = wave_sum(d);
-  float out[NR];
-  if (renorm) {
-    d -= w * inner;
+    const float inner = wave_sum(d);
+    float out[NR];
+    if (renorm) {
+      d -= w * inner;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) out[r] = 0.f;
-  } else {
-    float v[NR], local = -__builtin_inff();
+      for (int r = 0; r < NR; ++r) out[r] = 0.f;
+    } else {
+      float v[NR], local = -__builtin_inff();
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int i = r * 64 + lane;
+        v[r] = i < E ? logits[t * ldl + i] : -__builtin_inff();
+        local = fmaxf(local, v[r]);
+      }
+      float top = wave_max(local);
+      if (top == -__builtin_inff()) top = 0.f;
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        v[r] = expf(v[r] - top);
+        sum += v[r];
+      }
+      sum = wave_sum(sum);
+      const float scale = sum == 0.f ? 0.f : -inner / sum;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) out[r] = v[r] * scale;
+    }
+    for (int j = 0; j < k; ++j) {
+      const int ej = __builtin_amdgcn_readlane(e, j);
+      const float dj = lane_f32(d, j);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        if (r * 64 + lane == ej) out[r] += dj;
+    }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int i = r * 64 + lane;
-      v[r] = i < E ? logits[t * ldl + i] : -__builtin_inff();
-      local = fmaxf(local, v[r]);
+      if (i < E) dlogits[t * ldd + i] = out[r];
     }
-    float top = wave_max(local);
-    if (top == -__builtin_inff()) top = 0.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      v[r] = expf(v[r] - top);
-      sum += v[r];
-    }
-    sum = wave_sum(sum);
-    const float scale = sum == 0.f ? 0.f : -inner / sum;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) out[r] = v[r] * scale;
-  }
-  for (int j = 0; j < k; ++j) {
-    const int ej = __builtin_amdgcn_readlane(e, j);
-    const float dj = lane_f32(d, j);
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-      if (r * 64 + lane == ej) out[r] += dj;
-  }
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int i = r * 64 + lane;
-    if (i < E) dlogits[t * ldd + i] = out[r];
   }
 }
 
@@ -355,98 +439,154 @@ struct RowVec<4> {
   }
 };
 
+// Slots whose places are read at once, so that a batch of rows is in flight.
+constexpr int kSlotBatch = 8;
+
+// STREAM: the sorted rows pass the caches by (see stream_rows).
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_row(const u32x4* p) {
+  return STREAM ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_row(const u32x4& v, u32x4* p) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 // out[positions[t, j]] = a[t], zeros past the routed rows.
-template <int BYTES>
+template <int BYTES, bool STREAM>
 __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2;
-  if (t >= p.T) return;
   const int routed = *p.routed;
   const int lanes = 1 << p.lanes_log2, l = threadIdx.x & (lanes - 1);
   const int chunks = p.H * BYTES / 16;
-  for (int c = l; c < chunks; c += lanes) {
-    const u32x4 v = ((const u32x4*)((const char*)p.a + t * p.lda * BYTES))[c];
-    for (int j = 0; j < p.k; ++j) {
-      const int at = p.positions[t * p.k + j];
-      if ((uint64_t)(int64_t)at >= (uint64_t)p.R) continue;
-      ((u32x4*)((char*)p.out + at * p.ldo * BYTES))[c] = at < routed ? v : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-}
-
-// out[t] = sum_j weights[t, j] b[positions[t, j]], in ascending j and FP32.
-template <int IN, int OUT>
-__global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2;
-  if (t >= p.T) return;
-  const int64_t routed = min((int64_t)*p.routed, p.R);
-  const int lanes = 1 << p.lanes_log2, l = threadIdx.x & (lanes - 1);
-  constexpr int N = 8;  // columns of a thread's step
-  for (int c = l * N; c < p.H; c += lanes * N) {
-    float acc[N];
+  for (int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2; t < p.T;
+       t += ((int64_t)gridDim.x * 256) >> p.lanes_log2) {
+    for (int c = l; c < chunks; c += lanes) {
+      const u32x4 v = ((const u32x4*)((const char*)p.a + t * p.lda * BYTES))[c];
+      for (int j0 = 0; j0 < p.k; j0 += kSlotBatch) {
+        int at[kSlotBatch];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int at = p.positions[t * p.k + j];
-      if (at < 0 || at >= routed) continue;
-      const float w = p.weights ? p.weights[t * p.k + j] : 1.f;
-      const char* row = (const char*)p.b + (at * p.ldb + c) * IN;
+        for (int j = 0; j < kSlotBatch; ++j) at[j] = j0 + j < p.k ? p.positions[t * p.k + j0 + j] : -1;
 #pragma unroll
-      for (int q = 0; q < N / RowVec<IN>::N; ++q) {
-        float f[RowVec<IN>::N];
-        RowVec<IN>::unpack(((const u32x4*)row)[q], f);
-#pragma unroll
-        for (int i = 0; i < RowVec<IN>::N; ++i) acc[q * RowVec<IN>::N + i] += w * f[i];
-      }
-    }
-    char* out = (char*)p.out + (t * p.ldo + c) * OUT;
-#pragma unroll
-    for (int q = 0; q < N / RowVec<OUT>::N; ++q) {
-      float f[RowVec<OUT>::N];
-#pragma unroll
-      for (int i = 0; i < RowVec<OUT>::N; ++i) f[i] = acc[q * RowVec<OUT>::N + i];
-      ((u32x4*)out)[q] = RowVec<OUT>::pack(f);
-    }
-  }
-}
-
-// Gradients of the combination, one wave per token: out[positions[t, j]] =
-// weights[t, j] a[t] (zeros past the routed rows) and dweights[t, j] =
-// <a[t], b[positions[t, j]]>, a the incoming gradient.
-template <int BYTES>
-__global__ void __launch_bounds__(256) combine_dgrad_kernel(RowsParams p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.T) return;
-  const int64_t routed = min((int64_t)*p.routed, p.R);
-  constexpr int N = RowVec<BYTES>::N;
-  const int chunks = p.H / N;
-  const u32x4* dy = (const u32x4*)((const char*)p.a + t * p.lda * BYTES);
-  for (int j = 0; j < p.k; ++j) {
-    const int at = __builtin_amdgcn_readfirstlane(p.positions[t * p.k + j]);
-    float dot = 0.f;
-    if (at >= 0 && at < p.R) {
-      const bool live = at < routed;
-      const float w = live ? p.weights[t * p.k + j] : 0.f;
-      const u32x4* row = (const u32x4*)((const char*)p.b + (int64_t)at * p.ldb * BYTES);
-      u32x4* out = (u32x4*)((char*)p.out + (int64_t)at * p.ldo * BYTES);
-      for (int c = lane; c < chunks; c += 64) {
-        float f[N], g[N];
-        RowVec<BYTES>::unpack(dy[c], f);
-        if (live) {
-          RowVec<BYTES>::unpack(row[c], g);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot += f[i] * g[i];
-            f[i] *= w;
-          }
-          out[c] = RowVec<BYTES>::pack(f);
-        } else {
-          out[c] = u32x4{0u, 0u, 0u, 0u};
+        for (int j = 0; j < kSlotBatch; ++j) {
+          if ((uint64_t)(int64_t)at[j] >= (uint64_t)p.R) continue;
+          store_row<STREAM>(at[j] < routed ? v : u32x4{0u, 0u, 0u, 0u},
+                            (u32x4*)((char*)p.out + at[j] * p.ldo * BYTES) + c);
         }
       }
     }
+  }
+}
+
+// out[t] = sum_j weights[t, j] b[positions[t, j]], in ascending j and FP32.  A
+// batch's rows are all loaded before the first is used; where a slot has no
+// row the first one is read and nothing of it taken.
+template <int IN, int OUT, bool STREAM>
+__global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
+  const int64_t routed = min((int64_t)*p.routed, p.R);
+  const int lanes = 1 << p.lanes_log2, l = threadIdx.x & (lanes - 1);
+  constexpr int N = 8;                  // columns of a thread's step
+  constexpr int Q = N / RowVec<IN>::N;  // its loads of one row
+  for (int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2; t < p.T;
+       t += ((int64_t)gridDim.x * 256) >> p.lanes_log2) {
+    for (int c = l * N; c < p.H; c += lanes * N) {
+      float acc[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = 0.f;
+      for (int j0 = 0; j0 < p.k && routed > 0; j0 += kSlotBatch) {
+        int at[kSlotBatch];
+        float w[kSlotBatch];
+        u32x4 v[kSlotBatch][Q];
+#pragma unroll
+        for (int j = 0; j < kSlotBatch; ++j) {
+          at[j] = j0 + j < p.k ? p.positions[t * p.k + j0 + j] : -1;
+          w[j] = p.weights && j0 + j < p.k ? p.weights[t * p.k + j0 + j] : 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kSlotBatch; ++j) {
+          const bool live = at[j] >= 0 && at[j] < routed;
+          const char* row = (const char*)p.b + ((live ? at[j] : 0) * p.ldb + c) * IN;
+          if (j0 + j < p.k)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) v[j][q] = load_row<STREAM>((const u32x4*)row + q);
+          at[j] = live;
+        }
+#pragma unroll
+        for (int j = 0; j < kSlotBatch; ++j) {
+          if (j0 + j >= p.k) break;
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            float f[RowVec<IN>::N];
+            RowVec<IN>::unpack(v[j][q], f);
+#pragma unroll
+            for (int i = 0; i < RowVec<IN>::N; ++i)
+              acc[q * RowVec<IN>::N + i] = at[j] ? acc[q * RowVec<IN>::N + i] + w[j] * f[i] : acc[q * RowVec<IN>::N + i];
+          }
+        }
+      }
+      char* out = (char*)p.out + (t * p.ldo + c) * OUT;
+#pragma unroll
+      for (int q = 0; q < N / RowVec<OUT>::N; ++q) {
+        float f[RowVec<OUT>::N];
+#pragma unroll
+        for (int i = 0; i < RowVec<OUT>::N; ++i) f[i] = acc[q * RowVec<OUT>::N + i];
+        ((u32x4*)out)[q] = RowVec<OUT>::pack(f);
+      }
+    }
+  }
+}
+
+// Gradients of the combination, one wave per slot: out[positions[t, j]] =
+// weights[t, j] a[t] (zeros past the routed rows) and dweights[t, j] =
+// <a[t], b[positions[t, j]]>, a the incoming gradient.  The waves of a token
+// follow each other, so that its row of a comes from the cache but once.
+template <int BYTES, bool STREAM>
+__global__ void __launch_bounds__(256) combine_dgrad_kernel(RowsParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t routed = min((int64_t)*p.routed, p.R);
+  constexpr int N = RowVec<BYTES>::N, U = 4;  // U: chunks loaded together
+  const int chunks = p.H / N;
+  for (int64_t slot = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); slot < p.T * p.k;
+       slot += (int64_t)gridDim.x * 4) {
+    const int64_t t = slot / p.k;
+    const int at = __builtin_amdgcn_readfirstlane(p.positions[slot]);
+    float dot = 0.f;
+    if (at >= 0 && at < p.R) {
+      const u32x4* dy = (const u32x4*)((const char*)p.a + t * p.lda * BYTES);
+      const u32x4* row = (const u32x4*)((const char*)p.b + (int64_t)at * p.ldb * BYTES);
+      u32x4* out = (u32x4*)((char*)p.out + (int64_t)at * p.ldo * BYTES);
+      if (at < routed) {
+        const float w = p.weights[slot];
+        for (int c0 = lane; c0 < chunks; c0 += 64 * U) {
+          u32x4 a[U], b[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int c = min(c0 + 64 * u, chunks - 1);
+            a[u] = dy[c];
+            b[u] = load_row<STREAM>(row + c);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (c0 + 64 * u >= chunks) break;
+            float f[N], g[N];
+            RowVec<BYTES>::unpack(a[u], f);
+            RowVec<BYTES>::unpack(b[u], g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot += f[i] * g[i];
+              f[i] *= w;
+            }
+            store_row<STREAM>(RowVec<BYTES>::pack(f), out + c0 + 64 * u);
+          }
+        }
+      } else {
+        for (int c = lane; c < chunks; c += 64) store_row<STREAM>(u32x4{0u, 0u, 0u, 0u}, out + c);
+      }
+    }
     dot = wave_sum(dot);
-    if (lane == 0) p.dweights[t * p.k + j] = dot;
+    if (lane == 0) p.dweights[slot] = dot;
   }
 }
 

@@ -357,8 +357,9 @@ dpg_status dpg_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_
  *              row, by (expert, slot); the unused slots follow in order
  *   positions: int32 [T, top_k], the inverse: each slot's row
  * Pointers are 4-byte aligned.  1 <= top_k <= min(E, 32), E <= 512, T * top_k
- * below 2^31 (DPG_ERR_UNSUPPORTED beyond).  Workspace:
- * dpg_route_workspace_size (0 up to 64 tokens, one launch).
+ * below 2^31 and T at most 33521664 (DPG_ERR_UNSUPPORTED beyond).  Workspace:
+ * dpg_route_workspace_size bytes, 16-byte aligned (0 up to 64 tokens, one
+ * launch).
  */
 size_t dpg_route_workspace_size(int64_t T, int64_t E, int64_t top_k);
 dpg_status dpg_route(const float* logits, int64_t ldl, int64_t T, int64_t E, int64_t top_k, int renormalize,

@@ -183,7 +183,7 @@ def _case(T, k, H, E, dtype, seed=0, pad=0):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,k,H,E,pad", [(1, 1, 8, 1, 0), (3, 2, 24, 4, 8), (50, 6, 264, 9, 0), (130, 8, 4096, 64, 0),
-                                         (7, 4, 10240, 8, 16), (40, 32, 128, 40, 0)])
+                                         (7, 4, 10240, 8, 16), (40, 32, 128, 40, 0), (530, 8, 4104, 64, 0)])
 def test_rows_there_and_back(T, k, H, E, pad, dtype):
     r, rows = _case(T, k, H, E, dtype, pad=pad)
     used, pos = int(r.offsets[-1]), r.positions.long()
