@@ -8,6 +8,13 @@ checkpointed training step of a projection (forward, recomputed forward, input
 gradient, weight gradient) with static buffers and captures them in one HIP
 graph, so a replay costs no host work per kernel.
 
+``route``, ``dispatch``, ``grouped_projection`` and ``combine`` are the same for
+the expert layer's entry points; an expert layer is
+
+    r = route(router_gating(x32, w_router), top_k)
+    h = grouped_projection(dispatch(x, r), w_experts, r.offsets)
+    y = combine(h, r)
+
 Argument marshalling only, as in the rest of the package: every product runs
 in the library's kernels.  ``deterministic=False`` asks for the fast plans; when
 ``torch.use_deterministic_algorithms(True)`` is in force the deterministic
@@ -17,6 +24,8 @@ import warnings
 
 import torch
 
+from . import (Route, dpg_combine, dpg_combine_dgrad, dpg_dispatch, dpg_grouped_dgrad, dpg_grouped_forward,
+               dpg_grouped_wgrad, dpg_route, dpg_route_dgrad)
 from . import (dpg_dgrad, dpg_forward, dpg_router_dgrad, dpg_router_forward, dpg_router_wgrad, dpg_wgrad,
                workspace_size, PASS_FORWARD, PASS_DGRAD, PASS_WGRAD)
 
@@ -109,6 +118,86 @@ def router_gating(x, w, deterministic=True):
     """FP32 router logits y[..., E] = x[..., H] w[E, H]^T by BF16x3;
     differentiable in x and w (FP32 gradients)."""
     return _Router.apply(x, w, resolve_deterministic(deterministic))
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, renormalize):
+        r = dpg_route(logits, top_k, renormalize=renormalize)
+        ctx.save_for_backward(logits, r.experts, r.weights)
+        ctx.renormalize = renormalize
+        ctx.mark_non_differentiable(r.experts, r.offsets, r.rows, r.positions)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, _experts, dweights, _offsets, _rows_, _positions):
+        logits, experts, weights = ctx.saved_tensors
+        return dpg_route_dgrad(logits, experts, weights, dweights.contiguous(), renormalize=ctx.renormalize), None, None
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, offsets):
+        ctx.save_for_backward(positions, offsets)
+        return dpg_dispatch(x, positions, offsets)
+
+    @staticmethod
+    def backward(ctx, dxs):
+        positions, offsets = ctx.saved_tensors
+        return dpg_combine(_rows(dxs), positions, offsets), None, None
+
+
+class _Grouped(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return dpg_grouped_forward(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = _rows(dy)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = dpg_grouped_dgrad(dy, w, offsets)
+        if ctx.needs_input_grad[1]:
+            dw = dpg_grouped_wgrad(dy, x, offsets)
+        return dx, dw, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, positions, offsets):
+        ctx.save_for_backward(ys, weights, positions, offsets)
+        return dpg_combine(ys, positions, offsets, weights)
+
+    @staticmethod
+    def backward(ctx, dy):
+        ys, weights, positions, offsets = ctx.saved_tensors
+        return (*dpg_combine_dgrad(_rows(dy), ys, positions, offsets, weights), None, None)
+
+
+def route(logits, top_k, renormalize=True):
+    """dpg_route, differentiable from its weights to the logits (the choice of
+    experts is held)."""
+    return Route._make(_Route.apply(logits, top_k, bool(renormalize)))
+
+
+def dispatch(x, r):
+    """x [T, H] into the order of the route r, [T * top_k, H]; differentiable in x."""
+    return _Dispatch.apply(x, r.positions, r.offsets)
+
+
+def grouped_projection(x, w, offsets):
+    """y[r] = x[r] w[e]^T for the rows r of group e (BF16); differentiable in x and
+    w.  Use dpg_grouped_wgrad with out_dtype=torch.float32 for FP32 gradients."""
+    return _Grouped.apply(x, w, offsets)
+
+
+def combine(ys, r):
+    """y[t] = sum_j weights[t, j] ys[positions[t, j]]; differentiable in ys and in
+    the route's weights."""
+    return _Combine.apply(ys, r.weights, r.positions, r.offsets)
 
 
 class CheckpointedStep:
