@@ -22,8 +22,11 @@
 namespace dpg {
 
 constexpr int kAdamwBlock = 256;                  // elements of one scale: 4 per lane of a wave
-constexpr int kAdamwSteps = 4;                    // blocks of one wave, loaded before the first is worked on
-constexpr int kAdamwChunk = 4 * kAdamwSteps * kAdamwBlock;  // elements of a workgroup's four waves
+// Blocks of one wave, loaded before the first is worked on: four, or one where
+// a call has few elements and each wave's own time counts.
+constexpr int kAdamwSteps = 4;
+// elements of a workgroup's four waves
+constexpr int adamw_chunk(int steps) { return 4 * steps * kAdamwBlock; }
 constexpr int kAdamwTensors = 48;                 // tensors of one launch: 3.5 KB of kernel arguments
 
 struct AdamwTensor {
@@ -234,7 +237,7 @@ __device__ __forceinline__ void adamw_update(const AdamwParams& p, const AdamwTe
   }
 }
 
-template <int GRAD_BYTES, bool E4M3>
+template <int GRAD_BYTES, bool E4M3, int STEPS>
 __global__ void __launch_bounds__(256) adamw_kernel(AdamwParams p) {
   int lo = 0, hi = p.count;  // the tensor of this workgroup: the last one that starts at it or before
   while (hi - lo > 1) {
@@ -246,20 +249,21 @@ __global__ void __launch_bounds__(256) adamw_kernel(AdamwParams p) {
   }
   const AdamwTensor t = p.t[lo];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t first = (int64_t)((int)blockIdx.x - p.chunk0[lo]) * kAdamwChunk + wave * (kAdamwSteps * kAdamwBlock);
+  const int64_t first = (int64_t)((int)blockIdx.x - p.chunk0[lo]) * adamw_chunk(STEPS) +
+                        wave * (STEPS * kAdamwBlock);
   const float gs = p.grad_scale ? *p.grad_scale : 1.f;
   // whole quads through 16-byte (FP32), 8-byte (BF16) and 4-byte (codes)
   // accesses where the tensor's pointers allow them
   const uintptr_t low = (uintptr_t)t.p | (E4M3 ? ((uintptr_t)t.m | (uintptr_t)t.v) << 2 : (uintptr_t)t.m | (uintptr_t)t.v) |
                         ((uintptr_t)t.w << 1) | (GRAD_BYTES == 2 ? (uintptr_t)t.g << 1 : (uintptr_t)t.g);
   const bool wide = (low & 15) == 0;
-  AdamwQuad q[kAdamwSteps];
+  AdamwQuad q[STEPS];
 #pragma unroll
-  for (int s = 0; s < kAdamwSteps; ++s)
+  for (int s = 0; s < STEPS; ++s)
     if (first + s * kAdamwBlock < t.n)
       adamw_fetch<GRAD_BYTES, E4M3>(t, first + s * kAdamwBlock, lane, wide, q[s]);
 #pragma unroll
-  for (int s = 0; s < kAdamwSteps; ++s) {
+  for (int s = 0; s < STEPS; ++s) {
     if (first + s * kAdamwBlock >= t.n) return;
     adamw_update<E4M3>(p, t, p.key[lo], gs, first + s * kAdamwBlock, lane, wide, q[s]);
   }

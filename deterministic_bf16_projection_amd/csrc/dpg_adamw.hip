@@ -11,13 +11,17 @@ namespace {
 
 // workgroups of one launch: below 2^32 threads
 constexpr int64_t kMaxChunks = 1 << 23;
+// Calls of up to so many elements give a wave one block of 256 instead of four:
+// 1.8 million elements with 8-bit moments 12.8 -> 9.4 us, 4 million 20.3 -> 18.0;
+// with 32-bit moments 1.5 million 10.9 -> 9.8, but 4 million 19.7 -> 20.5.
+constexpr int64_t kFewElements[2] = {2 << 20, 4 << 20};  // 32-bit, 8-bit moments
 
 bool aligned_to(const void* p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
 dpg_status check_adamw(const dpg_adamw_tensor& t, int grad_dtype, bool e4m3) {
   if (t.numel < 0) return DPG_ERR_INVALID_ARG;
   if (t.numel == 0) return DPG_OK;
-  if (t.numel > kMaxChunks * kAdamwChunk) return DPG_ERR_UNSUPPORTED;
+  if (t.numel > kMaxChunks * adamw_chunk(kAdamwSteps)) return DPG_ERR_UNSUPPORTED;
   if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return DPG_ERR_INVALID_ARG;
   if (e4m3 && (!t.avg_scale || !t.sq_scale)) return DPG_ERR_INVALID_ARG;
   if (!aligned_to(t.param, 4) || !aligned_to(t.grad, grad_dtype == DPG_F32 ? 4 : 2) || !aligned_to(t.copy, 2))
@@ -26,6 +30,12 @@ dpg_status check_adamw(const dpg_adamw_tensor& t, int grad_dtype, bool e4m3) {
            : !aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))
     return DPG_ERR_ALIGNMENT;
   return DPG_OK;
+}
+
+template <int STEPS>
+const void* adamw_fn(bool bf16, bool e4m3) {
+  if (bf16) return e4m3 ? (const void*)&adamw_kernel<2, true, STEPS> : (const void*)&adamw_kernel<2, false, STEPS>;
+  return e4m3 ? (const void*)&adamw_kernel<4, true, STEPS> : (const void*)&adamw_kernel<4, false, STEPS>;
 }
 
 }  // namespace
@@ -58,13 +68,16 @@ extern "C" dpg_status dpg_adamw(const dpg_adamw_tensor* tensors, int64_t count, 
   p.root_scale = (float)(1 / sqrt(1 - pow(o->beta2, (double)o->step)));
   p.eps = (float)o->eps;
   p.grad_scale = o->grad_scale;
-  const void* fn = o->grad_dtype == DPG_BF16
-                       ? (e4m3 ? (const void*)&adamw_kernel<2, true> : (const void*)&adamw_kernel<2, false>)
-                       : (e4m3 ? (const void*)&adamw_kernel<4, true> : (const void*)&adamw_kernel<4, false>);
+  int64_t elements = 0;
+  for (int64_t i = 0; i < count; ++i) elements += tensors[i].numel;
+  const bool few = elements <= kFewElements[e4m3];
+  const int chunk = adamw_chunk(few ? 1 : kAdamwSteps);
+  const bool bf16 = o->grad_dtype == DPG_BF16;
+  const void* fn = few ? adamw_fn<1>(bf16, e4m3) : adamw_fn<kAdamwSteps>(bf16, e4m3);
   void* args[] = {&p};
   int64_t chunks = 0;
   for (int64_t i = 0; i <= count; ++i) {
-    const int64_t more = i < count ? (tensors[i].numel + kAdamwChunk - 1) / kAdamwChunk : 0;
+    const int64_t more = i < count ? (tensors[i].numel + chunk - 1) / chunk : 0;
     if (p.count > 0 && (i == count || p.count == kAdamwTensors || chunks + more > kMaxChunks)) {
       const dpg_status st = launch(fn, chunks, 256, 0, args, stream);
       if (st != DPG_OK) return st;

@@ -97,7 +97,7 @@ GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K)
     const double tiles = wgrad ? (double)E * std::ceil((double)N / t.bm) * std::ceil((double)K / t.bn)
                                : row_tiles(t.bm) * std::ceil(cols / t.bn);
     const double steps = std::ceil(reduced / 64);
-    for (int s = 1; s <= 16; s *= 2) {
+    for (int s = 1; s <= 16; ++s) {
       if (s > 1 && (s > steps || s * outputs * 4 > (double)(1ll << 30))) break;
       const double rounds = tiles * s / slots, load = std::min(1.0, rounds);
       const double step = kStepAlone[layout][v] + (kStepFull[layout][v] - kStepAlone[layout][v]) * load;
@@ -199,6 +199,8 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus() * t.per_cu);
   // worth its microsecond where a workgroup takes several groups' units
   p.ordered = wgrad && E <= kOrderGroups && E > 1 && units > grid;
+  const auto in64 = [](int64_t bytes) { return (bytes & 63) == 0; };
+  p.stream = p.splits == 1 && in64((int64_t)(uintptr_t)c) && in64(ldc * out_elt) && (!wgrad || in64(stride * out_elt));
   void* args[] = {&p};
   if (p.splits == 1)
     return launch((const void*)lookup_grouped_kernel(plan.variant, layout, out), grid, t.threads, 0, args, stream);

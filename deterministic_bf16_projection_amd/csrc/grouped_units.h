@@ -29,6 +29,7 @@ struct GroupedParams : GemmParams {
   int groups;
   int rows;            // rows of the token-side matrices
   int ordered;         // weight gradient: groups by descending size
+  int stream;          // outputs of whole 64-byte pieces: non-temporal stores
 };
 
 typedef __attribute__((address_space(4))) const int const_int_t;

@@ -119,8 +119,6 @@ def dpg_adamw(params, grads, exp_avgs, exp_avg_sqs, lr, beta1=0.9, beta2=0.999, 
     random from `seed`, which the caller changes from step to step."""
     if not params:
         return
-    if grad_scale is not None:
-        grad_scale = grad_scale.reshape(-1)
     if stream is None:
         _binding.adamw(params, grads, exp_avgs, exp_avg_sqs, copies, avg_scales, sq_scales, grad_scale, lr, beta1,
                        beta2, eps, weight_decay, step, seed & 0xFFFFFFFF)
