@@ -27,20 +27,20 @@ struct GroupedTile {
 };
 
 // The variants: the large kernel's two tiles, then the few-row kernels (forward:
-// 64 rows by 16 columns or 32 by 32, input gradient: 16 by 128).
-enum Variant { TILE_256, TILE_128, ROWS_64X16, ROWS_32X32, ROWS_16X128 };
+// 16 rows by 16 columns or 32 by 32, input gradient: 16 by 128).
+enum Variant { TILE_256, TILE_128, ROWS_16X16, ROWS_32X32, ROWS_16X128 };
 constexpr GroupedTile kGroupedTiles[] = {
-    {256, 256, 512, 1}, {128, 128, 256, 2}, {64, 16, 512, 2}, {32, 32, 512, 2}, {16, 128, 512, 2}};
+    {256, 256, 512, 1}, {128, 128, 256, 2}, {16, 16, 512, 2}, {32, 32, 512, 2}, {16, 128, 512, 2}};
 
 template <int OUT>
 GroupedFn lookup_skinny_kernel(int variant) {
-  return variant == ROWS_64X16   ? &grouped_skinny_kernel<false, 4, 1, 4, OUT>
+  return variant == ROWS_16X16   ? &grouped_rows16_kernel<OUT>
          : variant == ROWS_32X32 ? &grouped_skinny_kernel<false, 2, 2, 3, OUT>
                                  : &grouped_skinny_kernel<true, 1, 8, 1, OUT>;
 }
 
 GroupedFn lookup_grouped_kernel(int variant, int layout, int out) {
-  if (variant >= ROWS_64X16)
+  if (variant >= ROWS_16X16)
     return out == DPG_F32 ? lookup_skinny_kernel<OUT_F32>(variant) : lookup_skinny_kernel<OUT_BF16>(variant);
   static const GroupedFn table[2][3][2] = {
       {{GroupedRow<256, 256, 2, 4, 0>::fns[0], GroupedRow<256, 256, 2, 4, 0>::fns[1]},
@@ -58,35 +58,40 @@ struct GroupedPlan {
 
 // The plan with the least estimated time, from the sizes alone (a CU count of
 // 256 whatever the device, so that the bits do not depend on it).  The
-// estimates are fitted to 470 timings of 80 sizes on an MI355X (64 to 2048 by
-// 128 to 4096, 1 to 256 groups, 1 to 65536 rows, each with every variant and 1
-// to 16 splits): the choice is 1.6% slower than the best one on average, where
-// always the best unsplit tile of the two is 1.9 times slower.  In us:
+// estimates are fitted to some 700 timings of 130 sizes on an MI355X (64 to
+// 2048 by 128 to 4096, 1 to 256 groups, 1 to 65536 rows, each with every variant
+// and several splits).  In us:
 //   tiles: a unit takes its steps of 64 (about 1 while few units run; more when
 //     they share the chip) and its epilogue; splitting adds a launch and the
 //     traffic of its planes.  For example a weight gradient of 30000 rows into
 //     512 x 512: 438 in 128-tiles, 40 with 16 splits; a forward of 1024 rows
 //     and 8 groups, 1024 x 4096: 66 and 33 with 4.
 //   few rows: each CU moves 38 GB/s (forward) or 72 (input gradient) through
-//     its unit's fragments.  A forward of 8 rows in 8 of 256 groups, 512 x
-//     4096: 11, in 128-tiles 65.
+//     its unit's fragments, or the memory its weights.  A forward of 8 rows in
+//     8 of 256 groups, 512 x 4096: 9.4, in 128-tiles 66; of 256 rows in 64
+//     groups, 1024 x 4096: 93, 121 and in 32-row units 107; of 1024 rows 167,
+//     126 and 148.
 // A weight gradient's longest group is taken to hold 1.3 times the mean.
 GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K) {
   GroupedPlan best = {TILE_128, 1};
   if (E == 0 || R == 0 || N == 0 || K == 0) return best;
   constexpr double kCus = kDetCus, kStart = 4.6;  // us
-  // bytes of weights per us from memory: tiles of the forward (fetched into
-  // LDS) and of the input gradient, and the few-row kernels
-  const double tile_rate = layout == LAYOUT_FWD ? 4.6e6 : 5.4e6, rows_rate = 5.1e6;
   const bool wgrad = layout == LAYOUT_WGRAD;
-  const double groups = (double)std::min(E, R);  // with rows
+  const double groups =  // with rows: as many as R random ones reach
+      std::max(1.0, (double)E * (1 - std::exp(-(double)R / (double)E)));
   const double cols = (double)(layout == LAYOUT_FWD ? N : K), weights = groups * (double)N * (double)K * 2;
   const double reduced = wgrad ? 1.3 * (double)R / (double)E : (double)(layout == LAYOUT_FWD ? K : N);
   const double outputs = wgrad ? (double)E * (double)N * (double)K : (double)R * cols;
-  const auto row_tiles = [&](double bm) {
-    const double few = std::max(groups, std::ceil((double)R / bm));
-    return (double)R / groups > bm / 4 ? std::max(std::ceil((double)R / bm), (double)R / bm + 0.5 * groups) : few;
+  // row tiles: one a group, or `ends` parts of one more than the rows fill
+  const auto row_tiles = [&](double bm, double ends) {
+    const double filled = std::ceil((double)R / bm);
+    return (double)R / groups > bm / 4 ? std::max(filled, (double)R / bm + ends * groups) : std::max(groups, filled);
   };
+  // bytes of weights per us from memory: the tiles, and the few-row kernels
+  // while most groups are one unit high
+  static constexpr double kTileRate[2][2] = {{4.45e6, 4.6e6}, {4.6e6, 5.7e6}};
+  const bool low = (double)R / groups <= 8;
+  const double rows_rate[3] = {low ? 6.0e6 : 5.0e6, 5.1e6, low ? 6.1e6 : 5.2e6};
   static constexpr double kStepAlone[3][2] = {{1.0, 0.64}, {1.11, 0.78}, {0.81, 0.67}};
   static constexpr double kStepFull[3][2] = {{1.61, 1.09}, {1.04, 0.97}, {1.65, 1.17}};
   static constexpr double kEpilogue[2] = {5.0, 2.9};
@@ -95,7 +100,7 @@ GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K)
     const GroupedTile& t = kGroupedTiles[v];
     const double slots = kCus * t.per_cu;
     const double tiles = wgrad ? (double)E * std::ceil((double)N / t.bm) * std::ceil((double)K / t.bn)
-                               : row_tiles(t.bm) * std::ceil(cols / t.bn);
+                               : row_tiles(t.bm, 0.5) * std::ceil(cols / t.bn);
     const double steps = std::ceil(reduced / 64);
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && (s > steps || s * outputs * 4 > (double)(1ll << 30))) break;
@@ -103,7 +108,7 @@ GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K)
       const double step = kStepAlone[layout][v] + (kStepFull[layout][v] - kStepAlone[layout][v]) * load;
       double us = kStart + (rounds < 3 ? std::max(1.0, std::ceil(rounds)) : rounds + 0.5) *
                                (std::ceil(steps / s) * step + kEpilogue[v]);
-      if (!wgrad) us = std::max(us, kStart + weights / tile_rate);
+      if (!wgrad) us = std::max(us, kStart + weights / kTileRate[layout][v]);
       if (s > 1) us += 1.8 + (s + 1) * outputs * 4 / 4.55e6;
       if (least == 0 || us < least) {
         least = us;
@@ -111,14 +116,14 @@ GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K)
       }
     }
   }
-  for (int v = ROWS_64X16; v <= ROWS_16X128 && !wgrad; ++v) {
+  for (int v = ROWS_16X16; v <= ROWS_16X128 && !wgrad; ++v) {
     if ((v == ROWS_16X128) != (layout == LAYOUT_DGRAD)) continue;
     const GroupedTile& t = kGroupedTiles[v];
-    const double tiles = row_tiles(t.bm);
+    const double tiles = row_tiles(t.bm, v == ROWS_32X32 ? 1.0 : 0.7);
     const double rows = std::min((double)t.bm, std::ceil((double)R / tiles));
     const double bytes = reduced * 2 * (rows + t.bn) + 26e3, rate = layout == LAYOUT_FWD ? 38e3 : 72e3;
     const double us = kStart + std::max(std::max(tiles * std::ceil(cols / t.bn) / kCus, 1.0) * bytes / rate,
-                                        weights / rows_rate);
+                                        weights / rows_rate[v - ROWS_16X16]);
     if (us < least) {
       least = us;
       best = {v, 1};
