@@ -314,7 +314,8 @@ int64_t dpg_plan_cache_capacity(void);
  *             The sizes need not be known on the host: a call never waits.
  *             Groups may be empty (their weight gradient is zeros).  Offsets
  *             outside [0, R] or descending give unspecified values in the
- *             output, never an access outside the operands.
+ *             output, never an access outside the operands.  They must not
+ *             change while the call runs: every wave reads them for itself.
  *   R       : rows of the token side.  Rows at offsets[E] and past it belong to
  *             no group: they are not read, and their output rows are zeros.
  *   stride_*: elements between groups' matrices, a multiple of 16 bytes (0: one
