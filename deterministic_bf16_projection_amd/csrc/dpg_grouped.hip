@@ -178,7 +178,11 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   p.c = c;
   p.lda = lda;
   p.ldb = ldb;
-  p.ldc = mc.rows > 1 ? ldc : mc.cols;  // of one row the stride is never used, whatever it is
+  // of one row the stride finds no element, whatever it is; the tiles' 32-bit
+  // offsets of the rows past it have to lie past it (256 rows by 2^20 columns
+  // by 4 bytes: below 2^31), however many columns there are
+  const int64_t one_row = std::min<int64_t>(mc.cols, 1 << 20);
+  p.ldc = mc.rows > 1 ? ldc : one_row;
   p.M = (int)(wgrad ? N : R);
   p.N = (int)(layout == LAYOUT_FWD ? N : K);
   p.K = (int)(layout == LAYOUT_FWD ? K : N);  // weight gradient: each group's rows
@@ -214,7 +218,7 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   if (!workspace || workspace_bytes < grouped_workspace(layout, plan, E, R, N, K) || !aligned16(workspace))
     return DPG_ERR_WORKSPACE;
   p.c = workspace;
-  p.ldc = p.N;
+  p.ldc = mc.rows > 1 ? mc.cols : one_row;
   p.split_stride = (int64_t)p.M * p.N;
   p.batch_c = p.split_stride * p.splits;
   st = launch((const void*)lookup_grouped_kernel(plan.variant, layout, DPG_F32), grid, t.threads, 0, args, stream);

@@ -669,7 +669,9 @@ struct FastGemm {
   // The same through buffer stores, whose descriptor ends with the tile's valid
   // rows, and whose offset is put past it in columns beyond N: no branches and
   // no 64-bit addresses, so that a block's stores go out while the next one
-  // passes the LDS buffer.  The rows of a tile span less than 2^31 bytes.
+  // passes the LDS buffer.  The rows of a tile span less than 2^31 bytes (ldc <
+  // 2^21), and the descriptor ends with the tile's own columns of its last row:
+  // those of a single row may be 2^31.
   // STREAM: non-temporal, where rows are multiples of 64 bytes (input gradient
   // of 44501 rows, 128 x 4096, BF16: 95 -> 83 us); elsewhere the pieces of a
   // line would reach memory one by one (120 x 3672: 168 us, 104 without).
@@ -686,7 +688,7 @@ struct FastGemm {
     const int ld = (int)ldc;
     const int rows = min(M - row0, BM);
     const rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(out + ((int64_t)row0 * ldc + col0) * ELT, (short)0,
-                                                        max(((rows - 1) * ld + (N - col0)) * ELT, 0), 0x00020000);
+                                                        max(((rows - 1) * ld + min(N - col0, BN)) * ELT, 0), 0x00020000);
     constexpr int CHUNK = 16 / ELT;  // elements of a lane's store
     constexpr int HALVES = EOUT == OUT_BF16 ? 1 : 2;
     uint32_t voff[HALVES];

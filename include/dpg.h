@@ -326,8 +326,9 @@ int64_t dpg_plan_cache_capacity(void);
  * call and on every MI355X.  Where there are few output tiles the reduction is
  * split (each group's rows, for wgrad) and the parts are added in order from
  * the workspace: dpg_grouped_workspace_size bytes, 0 where nothing is split.
- * Row strides of x, dy and w below 2^22 elements, R, N, K below 2^31 - 512 and
- * E below 2^24 (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an
+ * Row strides of x, dy and w below 2^22 elements and of outputs of more than one
+ * row below 2^21, R, N, K below 2^31 - 512 and E below 2^24
+ * (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an
  * empty reduction writes zeros.
  */
 size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K);
