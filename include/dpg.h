@@ -418,7 +418,10 @@ dpg_status dpg_combine_dgrad(const void* dy, int64_t lddy, const void* ys, int64
  *              codes, from `seed`, the tensor's place in the array and the
  *              element's place alone: the same call gives the same bits, and a
  *              caller changes the seed from step to step.  A positive sqrt(v)
- *              is not rounded to 0.  Zero codes with any finite scale start.
+ *              is not rounded to 0.  A moment that is infinite or NaN (a
+ *              gradient that is, or whose square is) is stored as NaN and stays
+ *              so; its block's scale is that of the other elements, which it
+ *              does not change.  Zero codes with any finite scale start.
  * Tensors are contiguous; any element alignment is taken (16-byte aligned ones
  * run wide), up to 2^35 elements each.  step >= 1, 0 <= beta < 1, lr, eps, weight_decay finite and >= 0,
  * else DPG_ERR_INVALID_ARG.  lr and step are host values: a captured call
