@@ -193,7 +193,9 @@ dpg_status dpg_dispatch(const void* x, int64_t ldx, const int32_t* positions, co
   const bool past = stream_rows(xs, ldxs, R, H, elt);
   const RowsFn fn = elt == 2 ? (past ? &dispatch_kernel<2, true> : &dispatch_kernel<2, false>)
                              : (past ? &dispatch_kernel<4, true> : &dispatch_kernel<4, false>);
-  return launch((const void*)fn, row_grid(T, 256 >> p.lanes_log2), 256, 0, args, stream);
+  // rows past the slots' share the tokens' threads: top_k of them to a token
+  return launch((const void*)fn, row_grid(std::max(T, (R + top_k - 1) / top_k), 256 >> p.lanes_log2), 256, 0, args,
+                stream);
 }
 
 dpg_status dpg_combine(const void* ys, int64_t ldys, dpg_dtype ys_dtype, const int32_t* positions,
@@ -262,7 +264,7 @@ dpg_status dpg_combine_dgrad(const void* dy, int64_t lddy, const void* ys, int64
   const bool past = stream_rows(ys, ldys, R, H, elt) && stream_rows(dys, lddys, R, H, elt);
   const RowsFn fn = elt == 2 ? (past ? &combine_dgrad_kernel<2, true> : &combine_dgrad_kernel<2, false>)
                              : (past ? &combine_dgrad_kernel<4, true> : &combine_dgrad_kernel<4, false>);
-  return launch((const void*)fn, row_grid(T * top_k, 4), 256, 0, args, stream);
+  return launch((const void*)fn, row_grid(std::max(T * top_k, R), 4), 256, 0, args, stream);
 }
 
 }  // extern "C"

@@ -391,8 +391,10 @@ __global__ void __launch_bounds__(256) route_dgrad_kernel(const float* logits, i
 // --------------------------------------------------------- moving rows --
 // The row kernels go token by token: a token's row is read once for all its
 // slots, and slot j's row lies at positions[t, j] of the sorted matrix.  Slots
-// without an expert have their places past offsets[E], where rows are written
-// as zeros and never read.  Positions come from device memory: one outside the
+// without an expert have their places past offsets[E], where rows are never
+// read and are written as zeros, all of them: by their own indexes, since the
+// matrix may have more rows than there are slots, and a caller's positions
+// need not name each.  Positions come from device memory: one outside the
 // matrix is left out.
 //
 // Bound by memory: 16384 tokens, 8 slots each, 4096 columns of BF16 take 207 us
@@ -460,14 +462,20 @@ __device__ __forceinline__ void store_row(const u32x4& v, u32x4* p) {
     *p = v;
 }
 
+// rows of the sorted matrix that slots have: offsets[E] of them, as far as they exist
+__device__ __forceinline__ int64_t routed_rows(const RowsParams& p) {
+  return min((int64_t)max(*p.routed, 0), p.R);
+}
+
 // out[positions[t, j]] = a[t], zeros past the routed rows.
 template <int BYTES, bool STREAM>
 __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
-  const int routed = *p.routed;
+  const int64_t routed = routed_rows(p);
   const int lanes = 1 << p.lanes_log2, l = threadIdx.x & (lanes - 1);
   const int chunks = p.H * BYTES / 16;
-  for (int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2; t < p.T;
-       t += ((int64_t)gridDim.x * 256) >> p.lanes_log2) {
+  const int64_t place = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lanes_log2;
+  const int64_t places = ((int64_t)gridDim.x * 256) >> p.lanes_log2;
+  for (int64_t t = place; t < p.T; t += places) {
     for (int c = l; c < chunks; c += lanes) {
       const u32x4 v = ((const u32x4*)((const char*)p.a + t * p.lda * BYTES))[c];
       for (int j0 = 0; j0 < p.k; j0 += kSlotBatch) {
@@ -476,13 +484,15 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
         for (int j = 0; j < kSlotBatch; ++j) at[j] = j0 + j < p.k ? p.positions[t * p.k + j0 + j] : -1;
 #pragma unroll
         for (int j = 0; j < kSlotBatch; ++j) {
-          if ((uint64_t)(int64_t)at[j] >= (uint64_t)p.R) continue;
-          store_row<STREAM>(at[j] < routed ? v : u32x4{0u, 0u, 0u, 0u},
-                            (u32x4*)((char*)p.out + at[j] * p.ldo * BYTES) + c);
+          if (at[j] < 0 || at[j] >= routed) continue;
+          store_row<STREAM>(v, (u32x4*)((char*)p.out + at[j] * p.ldo * BYTES) + c);
         }
       }
     }
   }
+  for (int64_t r = routed + place; r < p.R; r += places)
+    for (int c = l; c < chunks; c += lanes)
+      store_row<STREAM>(u32x4{0u, 0u, 0u, 0u}, (u32x4*)((char*)p.out + r * p.ldo * BYTES) + c);
 }
 
 // out[t] = sum_j weights[t, j] b[positions[t, j]], in ascending j and FP32.  A
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
 // row the first one is read and nothing of it taken.
 template <int IN, int OUT, bool STREAM>
 __global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
-  const int64_t routed = min((int64_t)*p.routed, p.R);
+  const int64_t routed = routed_rows(p);
   const int lanes = 1 << p.lanes_log2, l = threadIdx.x & (lanes - 1);
   constexpr int N = 8;                  // columns of a thread's step
   constexpr int Q = N / RowVec<IN>::N;  // its loads of one row
@@ -550,49 +560,49 @@ __global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
 template <int BYTES, bool STREAM>
 __global__ void __launch_bounds__(256) combine_dgrad_kernel(RowsParams p) {
   const int lane = threadIdx.x & 63;
-  const int64_t routed = min((int64_t)*p.routed, p.R);
+  const int64_t routed = routed_rows(p);
   constexpr int N = RowVec<BYTES>::N, U = 4;  // U: chunks loaded together
   const int chunks = p.H / N;
-  for (int64_t slot = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); slot < p.T * p.k;
-       slot += (int64_t)gridDim.x * 4) {
+  const int64_t place = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t places = (int64_t)gridDim.x * 4;
+  for (int64_t slot = place; slot < p.T * p.k; slot += places) {
     const int64_t t = slot / p.k;
     const int at = __builtin_amdgcn_readfirstlane(p.positions[slot]);
     float dot = 0.f;
-    if (at >= 0 && at < p.R) {
+    if (at >= 0 && at < routed) {
       const u32x4* dy = (const u32x4*)((const char*)p.a + t * p.lda * BYTES);
       const u32x4* row = (const u32x4*)((const char*)p.b + (int64_t)at * p.ldb * BYTES);
       u32x4* out = (u32x4*)((char*)p.out + (int64_t)at * p.ldo * BYTES);
-      if (at < routed) {
-        const float w = p.weights[slot];
-        for (int c0 = lane; c0 < chunks; c0 += 64 * U) {
-          u32x4 a[U], b[U];
+      const float w = p.weights[slot];
+      for (int c0 = lane; c0 < chunks; c0 += 64 * U) {
+        u32x4 a[U], b[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int c = min(c0 + 64 * u, chunks - 1);
-            a[u] = dy[c];
-            b[u] = load_row<STREAM>(row + c);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (c0 + 64 * u >= chunks) break;
-            float f[N], g[N];
-            RowVec<BYTES>::unpack(a[u], f);
-            RowVec<BYTES>::unpack(b[u], g);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              dot += f[i] * g[i];
-              f[i] *= w;
-            }
-            store_row<STREAM>(RowVec<BYTES>::pack(f), out + c0 + 64 * u);
-          }
+        for (int u = 0; u < U; ++u) {
+          const int c = min(c0 + 64 * u, chunks - 1);
+          a[u] = dy[c];
+          b[u] = load_row<STREAM>(row + c);
         }
-      } else {
-        for (int c = lane; c < chunks; c += 64) store_row<STREAM>(u32x4{0u, 0u, 0u, 0u}, out + c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c0 + 64 * u >= chunks) break;
+          float f[N], g[N];
+          RowVec<BYTES>::unpack(a[u], f);
+          RowVec<BYTES>::unpack(b[u], g);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot += f[i] * g[i];
+            f[i] *= w;
+          }
+          store_row<STREAM>(RowVec<BYTES>::pack(f), out + c0 + 64 * u);
+        }
       }
     }
     dot = wave_sum(dot);
     if (lane == 0) p.dweights[slot] = dot;
   }
+  for (int64_t r = routed + place; r < p.R; r += places)
+    for (int c = lane; c < chunks; c += 64)
+      store_row<STREAM>(u32x4{0u, 0u, 0u, 0u}, (u32x4*)((char*)p.out + r * p.ldo * BYTES) + c);
 }
 
 }  // namespace dpg

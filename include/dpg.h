@@ -385,7 +385,9 @@ dpg_status dpg_route_dgrad(const float* logits, int64_t ldl, const int32_t* expe
  *   combine_dgrad: dys[positions[t, j]] = weights[t, j] dy[t] (zeros at rows >=
  *             offsets[E]) and dweights[t, j] = <dy[t], ys[positions[t, j]]> (0
  *             for unused slots), summed in FP32
- * Matrices follow the conventions at the top (16-byte rows); BF16 or FP32, one
+ * Every row from offsets[E] on is written as zeros, whether a position names it
+ * or not (R may exceed T * top_k); a row before it that none names stays as it
+ * was.  T = 0 is a no-op: nothing is written.  Matrices follow the conventions at the top (16-byte rows); BF16 or FP32, one
  * type per call except that combine takes one for ys and one for y.  Positions
  * outside [0, R) are left out.
  */
