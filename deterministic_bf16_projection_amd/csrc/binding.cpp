@@ -196,6 +196,17 @@ T* data(const Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
+// A call has written to a caller's tensor: its version goes up, as after torch's
+// own in-place operations, so that a backward pass that saved it says so
+// instead of computing with the new values.  Inference tensors have no version
+// and are never saved.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* given, const Tensor& out) {
+  if (given != Py_None) written(out);
+}
+
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
 int64_t integer(PyObject* o, const char* name) {
@@ -250,6 +261,7 @@ PyObject* grouped_rows(PyObject* const* a, bool forward) {
                   row_stride(out, "out"), code_of(out.scalar_type()), data<int32_t>(off), E, R, N, K,
                   workspace_data(ws), workspace_bytes(ws), stream_of(x)),
                forward ? "dpg_grouped_forward" : "dpg_grouped_dgrad");
+  written(a[3], out);
   return wrap(std::move(out));
 }
 PyObject* grouped_forward(PyObject* const* a) { return grouped_rows(a, true); }
@@ -273,6 +285,7 @@ PyObject* grouped_wgrad(PyObject* const* a) {
                                  out.data_ptr(), g.row, g.group, code_of(out.scalar_type()), data<int32_t>(off), E, R,
                                  N, K, workspace_data(ws), workspace_bytes(ws), stream_of(dy)),
                "dpg_grouped_wgrad");
+  written(a[3], out);
   return wrap(std::move(out));
 }
 
@@ -344,6 +357,7 @@ PyObject* route_dgrad(PyObject* const* a) {
                                data<float>(dweights), data<float>(out), o.ld, l.T, l.E, k, renorm,
                                stream_of(logits)),
                "dpg_route_dgrad");
+  written(a[5], out);
   return wrap(std::move(out));
 }
 
@@ -364,6 +378,7 @@ PyObject* dispatch(PyObject* const* a) {
                             row_stride(out, "out"), code_of(x.scalar_type()), T, T * k, H, off.size(0) - 1, k,
                             stream_of(x)),
                "dpg_dispatch");
+  written(a[3], out);
   return wrap(std::move(out));
 }
 
@@ -388,6 +403,7 @@ PyObject* combine(PyObject* const* a) {
                            data<int32_t>(off), w, out.data_ptr(), row_stride(out, "out"), code_of(out.scalar_type()),
                            T, R, H, off.size(0) - 1, k, stream_of(ys)),
                "dpg_combine");
+  written(a[4], out);
   return wrap(std::move(out));
 }
 
@@ -436,12 +452,17 @@ class Column {
   void check_size(int64_t n) const {
     if (seq_ && size() != n) value_error(std::string(name_) + " must hold one tensor per parameter");
   }
-  void* pointer(int64_t i, at::ScalarType dtype, const Tensor& param, int64_t numel) const {
+  // the data of tensor i; one that the step writes is added to `outputs`
+  void* pointer(int64_t i, at::ScalarType dtype, at::Device device, int64_t numel,
+                std::vector<c10::TensorImpl*>* outputs = nullptr) const {
     if (!seq_) return nullptr;
     const Tensor& t = at(i);
+    if (outputs) outputs->push_back(t.unsafeGetTensorImpl());
     if (t.scalar_type() != dtype) type_error(std::string(name_) + " must be " + dtype_text(dtype));
-    if (!t.is_cuda()) value_error(std::string(name_) + " must be device tensors");
-    same_device(param, t, name_);
+    if (t.device() != device) {
+      if (!t.is_cuda()) value_error(std::string(name_) + " must be device tensors");
+      value_error(std::string(name_) + " is on " + t.device().str() + ", expected " + device.str());
+    }
     if (t.numel() != numel)
       value_error(std::string(name_) + ": " + std::to_string(t.numel()) + " elements, expected " +
                   std::to_string(numel));
@@ -474,38 +495,44 @@ PyObject* adamw(PyObject* const* a) {
   if (!e4m3 && state != at::kFloat) type_error("moments must be torch.float32 or torch.float8_e4m3fn");
   if (grad != at::kFloat && grad != at::kBFloat16) type_error("grads must be torch.bfloat16 or torch.float32");
   if (e4m3 && (!avg_scales.given() || !sq_scales.given())) value_error("8-bit moments need avg_scales and sq_scales");
-  std::vector<dpg_adamw_tensor> table(n);
-  for (int64_t i = 0; i < n; ++i) {
-    const Tensor& p = params.at(i);
-    const int64_t numel = p.numel(), blocks = (numel + kScaleBlock - 1) / kScaleBlock;
-    dpg_adamw_tensor& t = table[i];
-    t.param = (float*)params.pointer(i, at::kFloat, first, numel);
-    t.grad = grads.pointer(i, grad, first, numel);
-    t.exp_avg = avgs.pointer(i, state, first, numel);
-    t.exp_avg_sq = sqs.pointer(i, state, first, numel);
-    t.avg_scale = e4m3 ? (float*)avg_scales.pointer(i, at::kFloat, first, blocks) : nullptr;
-    t.sq_scale = e4m3 ? (float*)sq_scales.pointer(i, at::kFloat, first, blocks) : nullptr;
-    t.copy = copies.pointer(i, at::kBFloat16, first, numel);
-    t.numel = numel;
-  }
+  // numbers first: reading one may run Python code, and from here on tensors are held by address
   dpg_adamw_options o{};
-  if (a[7] != Py_None) {
-    const Tensor& s = packed(a[7], at::kFloat, "grad_scale");
-    if (s.numel() != 1) value_error("grad_scale must hold one value");
-    same_device(first, s, "grad_scale");
-    o.grad_scale = data<float>(s);
-  }
   o.lr = number(a[8], "lr");
   o.beta1 = number(a[9], "beta1");
   o.beta2 = number(a[10], "beta2");
   o.eps = number(a[11], "eps");
   o.weight_decay = number(a[12], "weight_decay");
   o.step = integer(a[13], "step");
+  o.seed = (uint32_t)integer(a[14], "seed");
+  std::vector<dpg_adamw_tensor> table(n);
+  std::vector<c10::TensorImpl*> outputs;
+  outputs.reserve(6 * n);
+  const at::Device device = first.device();
+  for (int64_t i = 0; i < n; ++i) {
+    const Tensor& p = params.at(i);
+    const int64_t numel = p.numel(), blocks = (numel + kScaleBlock - 1) / kScaleBlock;
+    dpg_adamw_tensor& t = table[i];
+    t.param = (float*)params.pointer(i, at::kFloat, device, numel, &outputs);
+    t.grad = grads.pointer(i, grad, device, numel);
+    t.exp_avg = avgs.pointer(i, state, device, numel, &outputs);
+    t.exp_avg_sq = sqs.pointer(i, state, device, numel, &outputs);
+    t.avg_scale = e4m3 ? (float*)avg_scales.pointer(i, at::kFloat, device, blocks, &outputs) : nullptr;
+    t.sq_scale = e4m3 ? (float*)sq_scales.pointer(i, at::kFloat, device, blocks, &outputs) : nullptr;
+    t.copy = copies.pointer(i, at::kBFloat16, device, numel, &outputs);
+    t.numel = numel;
+  }
+  if (a[7] != Py_None) {
+    const Tensor& s = packed(a[7], at::kFloat, "grad_scale");
+    if (s.numel() != 1) value_error("grad_scale must hold one value");
+    same_device(first, s, "grad_scale");
+    o.grad_scale = data<float>(s);
+  }
   o.grad_dtype = grad == at::kFloat ? DPG_F32 : DPG_BF16;
   o.state_dtype = e4m3 ? DPG_E4M3 : DPG_F32;
-  o.seed = (uint32_t)integer(a[14], "seed");
   const c10::DeviceGuard guard(first.device());
   check_status(dpg_adamw(table.data(), n, &o, stream_of(first)), "dpg_adamw");
+  for (c10::TensorImpl* t : outputs)
+    if (!t->is_inference()) t->bump_version();
   Py_RETURN_NONE;
 }
 

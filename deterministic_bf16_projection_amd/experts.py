@@ -2,8 +2,9 @@
 
 The entry points of ``include/dpg.h`` of the same names, in the manner of the
 package's projections: torch tensors in, outputs allocated on the call's stream
-where the caller gives none, errors raised before any launch.  The compiled
-module ``_binding`` checks and marshals the arguments; called through ctypes
+where the caller gives none, errors raised before any launch.  What a call
+writes in place (an ``out``, the optimizer's tensors) counts as modified for
+autograd.  The compiled module ``_binding`` checks and marshals the arguments; called through ctypes
 like the projections, it would take longer than the kernels of small calls.  A
 training step of an expert layer is
 
