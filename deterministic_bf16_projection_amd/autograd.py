@@ -15,6 +15,8 @@ the expert layer's entry points; an expert layer is
     h = grouped_projection(dispatch(x, r), w_experts, r.offsets)
     y = combine(h, r)
 
+Their gradients have no gradients: differentiating twice raises.
+
 Argument marshalling only, as in the rest of the package: every product runs
 in the library's kernels.  ``deterministic=False`` asks for the fast plans; when
 ``torch.use_deterministic_algorithms(True)`` is in force the deterministic
@@ -23,6 +25,7 @@ plans are used instead and a warning is given once.
 import warnings
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (Route, dpg_combine, dpg_combine_dgrad, dpg_dispatch, dpg_grouped_dgrad, dpg_grouped_forward,
                dpg_grouped_wgrad, dpg_route, dpg_route_dgrad)
@@ -130,6 +133,7 @@ class _Route(torch.autograd.Function):
         return tuple(r)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _experts, dweights, _offsets, _rows_, _positions):
         logits, experts, weights = ctx.saved_tensors
         return dpg_route_dgrad(logits, experts, weights, dweights.contiguous(), renormalize=ctx.renormalize), None, None
@@ -142,6 +146,7 @@ class _Dispatch(torch.autograd.Function):
         return dpg_dispatch(x, positions, offsets)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dxs):
         positions, offsets = ctx.saved_tensors
         return dpg_combine(_rows(dxs), positions, offsets), None, None
@@ -154,6 +159,7 @@ class _Grouped(torch.autograd.Function):
         return dpg_grouped_forward(x, w, offsets)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = _rows(dy)
@@ -172,6 +178,7 @@ class _Combine(torch.autograd.Function):
         return dpg_combine(ys, positions, offsets, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         ys, weights, positions, offsets = ctx.saved_tensors
         return (*dpg_combine_dgrad(_rows(dy), ys, positions, offsets, weights), None, None)
