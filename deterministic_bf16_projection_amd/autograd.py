@@ -123,33 +123,55 @@ def router_gating(x, w, deterministic=True):
     return _Router.apply(x, w, resolve_deterministic(deterministic))
 
 
+def _matrix(t):
+    """[..., C] as a 2-D matrix that the library takes: rows that do not overlap,
+    unit column stride; copied only where it is not one already."""
+    t2 = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    rows, cols = t2.shape
+    return t2 if (cols <= 1 or t2.stride(1) == 1) and (rows <= 1 or t2.stride(0) >= cols) else t2.contiguous()
+
+
+def _slots(t):
+    """[..., top_k] as [T, top_k]."""
+    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, renormalize):
-        r = dpg_route(logits, top_k, renormalize=renormalize)
-        ctx.save_for_backward(logits, r.experts, r.weights)
+        matrix = _matrix(logits)
+        r = dpg_route(matrix, top_k, renormalize=renormalize)
+        if logits.dim() != 2:
+            lead = logits.shape[:-1]
+            r = r._replace(experts=r.experts.view(*lead, top_k), weights=r.weights.view(*lead, top_k),
+                           positions=r.positions.view(*lead, top_k))
+        ctx.save_for_backward(matrix, r.experts, r.weights)
         ctx.renormalize = renormalize
+        ctx.shape = logits.shape
         ctx.mark_non_differentiable(r.experts, r.offsets, r.rows, r.positions)
         return tuple(r)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, _experts, dweights, _offsets, _rows_, _positions):
-        logits, experts, weights = ctx.saved_tensors
-        return dpg_route_dgrad(logits, experts, weights, dweights.contiguous(), renormalize=ctx.renormalize), None, None
+        matrix, experts, weights = ctx.saved_tensors
+        dlogits = dpg_route_dgrad(matrix, _slots(experts), _slots(weights), _slots(dweights).contiguous(),
+                                  renormalize=ctx.renormalize)
+        return dlogits.reshape(ctx.shape), None, None
 
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, positions, offsets):
         ctx.save_for_backward(positions, offsets)
-        return dpg_dispatch(x, positions, offsets)
+        ctx.shape = x.shape
+        return dpg_dispatch(_matrix(x), _slots(positions), offsets)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
         positions, offsets = ctx.saved_tensors
-        return dpg_combine(_rows(dxs), positions, offsets), None, None
+        return dpg_combine(_rows(dxs), _slots(positions), offsets).reshape(ctx.shape), None, None
 
 
 class _Grouped(torch.autograd.Function):
@@ -175,23 +197,26 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, positions, offsets):
         ctx.save_for_backward(ys, weights, positions, offsets)
-        return dpg_combine(ys, positions, offsets, weights)
+        y = dpg_combine(ys, _slots(positions), offsets, _slots(weights))
+        return y if positions.dim() == 2 else y.view(*positions.shape[:-1], ys.shape[1])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         ys, weights, positions, offsets = ctx.saved_tensors
-        return (*dpg_combine_dgrad(_rows(dy), ys, positions, offsets, weights), None, None)
+        dys, dweights = dpg_combine_dgrad(_rows(dy), ys, _slots(positions), offsets, _slots(weights))
+        return dys, dweights.view(weights.shape), None, None
 
 
 def route(logits, top_k, renormalize=True):
-    """dpg_route, differentiable from its weights to the logits (the choice of
-    experts is held)."""
+    """dpg_route on logits [..., E], differentiable from its weights to the logits
+    (the choice of experts is held): experts, weights and positions are [...,
+    top_k], the tokens numbered in the order of the leading dimensions."""
     return Route._make(_Route.apply(logits, top_k, bool(renormalize)))
 
 
 def dispatch(x, r):
-    """x [T, H] into the order of the route r, [T * top_k, H]; differentiable in x."""
+    """x [..., H] into the order of the route r, [T * top_k, H]; differentiable in x."""
     return _Dispatch.apply(x, r.positions, r.offsets)
 
 
@@ -202,8 +227,8 @@ def grouped_projection(x, w, offsets):
 
 
 def combine(ys, r):
-    """y[t] = sum_j weights[t, j] ys[positions[t, j]]; differentiable in ys and in
-    the route's weights."""
+    """y[t] = sum_j weights[t, j] ys[positions[t, j]], as [..., H] with the leading
+    dimensions of the route r; differentiable in ys and in the route's weights."""
     return _Combine.apply(ys, r.weights, r.positions, r.offsets)
 
 
