@@ -233,6 +233,9 @@ Tensor workspace_of(PyObject* o, size_t need, const Tensor& like) {
   const Tensor& t = tensor(o, "workspace");
   if (!t.is_cuda() || t.device() != like.device())
     value_error("workspace must be a device tensor on " + like.device().str());
+  // its bytes are counted from its first one: of a view with gaps they would be
+  // others' memory, of an expanded one no memory at all
+  if (!t.is_contiguous()) value_error("workspace must be contiguous");
   return t;
 }
 void* workspace_data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
