@@ -58,6 +58,8 @@ _lib.dpg_workspace_size.argtypes = [_ci, _i64, _i64, _i64, _ci, _ci, _ci]
 _lib.dpg_workspace_size.restype = _sz
 _lib.dpg_plan_describe.argtypes = [_ci, _i64, _i64, _i64, _ci, _ci, _ci, ctypes.c_char_p, _sz]
 _lib.dpg_plan_describe.restype = _ci
+_lib.dpg_grouped_plan_describe.argtypes = [_ci, _i64, _i64, _i64, _i64, ctypes.c_char_p, _sz]
+_lib.dpg_grouped_plan_describe.restype = _ci
 _lib.dpg_clear_plan_cache.argtypes = []
 _lib.dpg_clear_plan_cache.restype = None
 _lib.dpg_plan_cache_stats.argtypes = [ctypes.POINTER(_i64), ctypes.POINTER(_i64)]
@@ -177,6 +179,16 @@ def plan_describe(pass_, T, N, K, out_dtype=torch.bfloat16, deterministic=True, 
     st = _lib.dpg_plan_describe(pass_, T, N, K, _code(out_dtype), int(bool(deterministic)), split_k, buf, 1024)
     if st:
         raise DpgError(st, "dpg_plan_describe")
+    return buf.value.decode()
+
+
+def grouped_plan_describe(pass_, E, R, N, K):
+    """The plan of a grouped product of E groups and R rows (PASS_FORWARD,
+    PASS_DGRAD or PASS_WGRAD)."""
+    buf = ctypes.create_string_buffer(1024)
+    st = _lib.dpg_grouped_plan_describe(pass_, E, R, N, K, buf, 1024)
+    if st:
+        raise DpgError(st, "dpg_grouped_plan_describe")
     return buf.value.decode()
 
 

@@ -3,6 +3,8 @@
 // unit stream in grouped_units.h, the kernels in gemm_fast.h.
 #include <hip/hip_runtime.h>
 
+#include <stdio.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -138,6 +140,26 @@ size_t grouped_workspace(int layout, const GroupedPlan& plan, int64_t E, int64_t
   return (size_t)plan.splits * (size_t)elements * sizeof(float);
 }
 
+bool within_limits(int64_t E, int64_t R, int64_t N, int64_t K) {
+  return std::max(R, std::max(N, K)) < (1ll << 31) - 512 && E < (1ll << 24);
+}
+
+// The most units there can be: every group with rows may end in a part of a
+// tile, and so may the rows past the last group.
+int64_t grouped_units(int layout, const GroupedPlan& plan, int64_t E, int64_t R, int64_t N, int64_t K) {
+  const GroupedTile& t = kGroupedTiles[plan.variant];
+  const bool wgrad = layout == LAYOUT_WGRAD;
+  const int64_t cols = layout == LAYOUT_FWD ? N : K;
+  const int64_t tiles_m = wgrad ? E * ((N + t.bm - 1) / t.bm) : R / t.bm + std::min<int64_t>(E + 1, R);
+  return tiles_m * ((cols + t.bn - 1) / t.bn) * plan.splits;
+}
+
+// The weight gradient's groups by descending size: worth its microsecond where
+// a workgroup takes several groups' units.
+bool grouped_ordered(int layout, int64_t E, int64_t units, int64_t grid) {
+  return layout == LAYOUT_WGRAD && E <= kOrderGroups && E > 1 && units > grid;
+}
+
 // One grouped pass.  (a, b) are (x, w), (dy, w) and (dy, x); `stride` is the
 // element stride between the groups' weights (weight gradient: outputs).
 dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, int64_t ldb, void* c, int64_t ldc,
@@ -169,8 +191,7 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   if (E > 0 && (!offsets || ((uintptr_t)offsets & 3u))) return offsets ? DPG_ERR_ALIGNMENT : DPG_ERR_INVALID_ARG;
   // a tile is addressed through 32-bit buffer offsets, rows and units through 32-bit indexes
   if (std::max(lda, ldb) >= (1 << 22) || (mc.rows > 1 && ldc >= (1 << 21))) return DPG_ERR_UNSUPPORTED;
-  if (R >= (1ll << 31) - 512 || N >= (1ll << 31) - 512 || K >= (1ll << 31) - 512 || E >= (1ll << 24))
-    return DPG_ERR_UNSUPPORTED;
+  if (!within_limits(E, R, N, K)) return DPG_ERR_UNSUPPORTED;
 
   GroupedParams p{};
   p.a = a;
@@ -200,14 +221,10 @@ dpg_status run_grouped(int layout, const void* a, int64_t lda, const void* b, in
   p.kt_total = std::max(1, (p.K + 63) / 64);
   p.group_m = 4;
   p.splits = plan.splits;
-  // the most units there can be: every group with rows may end in a part of a
-  // tile, and so may the rows past the last group
-  const int64_t tiles_m = wgrad ? E * p.tiles_m : R / t.bm + std::min<int64_t>(E + 1, R);
-  const int64_t units = tiles_m * p.tiles_n * p.splits;
+  const int64_t units = grouped_units(layout, plan, E, R, N, K);
   if (units >= (1ll << 31) - (1 << 20)) return DPG_ERR_UNSUPPORTED;
   const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus() * t.per_cu);
-  // worth its microsecond where a workgroup takes several groups' units
-  p.ordered = wgrad && E <= kOrderGroups && E > 1 && units > grid;
+  p.ordered = grouped_ordered(layout, E, units, grid);
   const auto in64 = [](int64_t bytes) { return (bytes & 63) == 0; };
   p.stream = p.splits == 1 && in64((int64_t)(uintptr_t)c) && in64(ldc * out_elt) && (!wgrad || in64(stride * out_elt));
   void* args[] = {&p};
@@ -245,6 +262,25 @@ size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N
   const int layout = (int)pass;
   if (layout < LAYOUT_FWD || layout > LAYOUT_WGRAD || E < 0 || R < 0 || N < 0 || K < 0) return (size_t)-1;
   return grouped_workspace(layout, grouped_plan(layout, E, R, N, K), E, R, N, K);
+}
+
+dpg_status dpg_grouped_plan_describe(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K, char* buf,
+                                     size_t buflen) {
+  static const char* kPass[] = {"forward", "dgrad", "wgrad"};
+  const int layout = (int)pass;
+  if (!buf || buflen == 0) return DPG_ERR_INVALID_ARG;
+  if (layout < LAYOUT_FWD || layout > LAYOUT_WGRAD || E < 0 || R < 0 || N < 0 || K < 0) return DPG_ERR_INVALID_ARG;
+  // (so that the units fit 64 bits)
+  if (!within_limits(E, R, N, K) || (double)E * (double)N * (double)K >= 0x1p62) return DPG_ERR_UNSUPPORTED;
+  const GroupedPlan plan = grouped_plan(layout, E, R, N, K);
+  const GroupedTile& t = kGroupedTiles[plan.variant];
+  const int64_t units = grouped_units(layout, plan, E, R, N, K);
+  const int64_t grid = std::min<int64_t>(units, (int64_t)kDetCus * t.per_cu);
+  snprintf(buf, buflen, "pass=%s kind=grouped kernel=%s tile=%dx%d threads=%d splits=%d units=%lld grid=%lld ordered=%d "
+           "workspace=%zu", kPass[layout], plan.variant >= ROWS_16X16 ? "few_rows" : "pipelined", t.bm, t.bn, t.threads,
+           plan.splits, (long long)units, (long long)grid, (int)grouped_ordered(layout, E, units, grid),
+           grouped_workspace(layout, plan, E, R, N, K));
+  return DPG_OK;
 }
 
 dpg_status dpg_grouped_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, void* y,

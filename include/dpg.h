@@ -332,6 +332,11 @@ int64_t dpg_plan_cache_capacity(void);
  * empty reduction writes zeros.
  */
 size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K);
+/* Host-only description of a grouped call's plan (kernel, tile, K splits, the
+ * most units there can be and the grid on 256 CUs, whether the weight gradient
+ * takes its groups by size, workspace), as dpg_plan_describe. */
+dpg_status dpg_grouped_plan_describe(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K, char* buf,
+                                     size_t buflen);
 dpg_status dpg_grouped_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, void* y,
                                int64_t ldy, dpg_dtype y_dtype, const int32_t* offsets, int64_t E, int64_t R,
                                int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream);
