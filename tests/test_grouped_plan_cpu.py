@@ -3,6 +3,8 @@ import ctypes
 
 import pytest
 
+import tile_cases
+
 dpg = pytest.importorskip("deterministic_bf16_projection_amd")
 
 I = ctypes.c_int64
@@ -45,3 +47,27 @@ def test_description_refusals():
         dpg.grouped_plan_describe(dpg.PASS_FORWARD, 1, -1, 8, 8)
     for args in ((0, 0, 0, 0), (1, 0, 64, 64), (0, 50, 64, 64)):
         assert plan(dpg.PASS_WGRAD, *args)["splits"] == "1"
+
+
+@pytest.mark.parametrize("case", tile_cases.TILES, ids=tile_cases.ident)
+def test_the_tile_cases_take_their_kernels(case):
+    """The sizes that test_gpu_grouped_tiles.py runs reach the kernels they stand for."""
+    pass_, counts, tail, N, K, tile, ordered = case
+    p = plan(("forward", "dgrad", "wgrad").index(pass_), len(counts), sum(counts) + tail, N, K)
+    assert (p["kernel"], p["tile"], p["splits"]) == ("pipelined", tile, "1")
+    if ordered is not None:
+        assert p["ordered"] == str(ordered)
+        if len(counts) > 256:  # not ordered, and several rounds of the grid
+            assert int(p["units"]) > int(p["grid"])
+
+
+def test_the_tile_cases_cover_every_kernel():
+    seen = {(c[0], c[5], c[6]) for c in tile_cases.TILES}
+    assert seen == {(p, t, None) for p in ("forward", "dgrad") for t in ("256x256", "128x128")} | {
+        ("wgrad", t, o) for t in ("256x256", "128x128") for o in (0, 1)}
+
+
+@pytest.mark.parametrize("N", [1 << 24, (1 << 29) + 1032])
+def test_one_wide_row_takes_a_tile(N):
+    p = plan(dpg.PASS_FORWARD, 1, 1, N, 8)
+    assert (p["kernel"], p["splits"]) == ("pipelined", "1")
