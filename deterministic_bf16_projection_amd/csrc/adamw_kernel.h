@@ -115,7 +115,7 @@ struct AdamwQuad {
 // Everything is read and written once: non-temporal accesses.  201 million
 // parameters, 32-bit moments, BF16 gradients and copies: 1064 us without, 980
 // with, and 952 (5.9 TB/s) with four blocks of a wave in flight instead of one;
-// 8-bit moments and FP32 gradients 692, 660 and 662 (5.5 TB/s).
+// 8-bit moments and FP32 gradients 692, 660 and 655 (5.5 TB/s).
 template <class T>
 __device__ __forceinline__ T adamw_load(const void* p) {
   return __builtin_nontemporal_load((const T*)p);

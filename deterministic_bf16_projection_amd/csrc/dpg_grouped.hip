@@ -70,8 +70,8 @@ struct GroupedPlan {
 //     and 8 groups, 1024 x 4096: 66 and 33 with 4.
 //   few rows: each CU moves 38 GB/s (forward) or 72 (input gradient) through
 //     its unit's fragments, or the memory its weights.  A forward of 8 rows in
-//     8 of 256 groups, 512 x 4096: 9.4, in 128-tiles 66; of 256 rows in 64
-//     groups, 1024 x 4096: 93, 121 and in 32-row units 107; of 1024 rows 167,
+//     8 of 256 groups, 512 x 4096: 8.6, in 128-tiles 66; of 256 rows in 64
+//     groups, 1024 x 4096: 90, 121 and in 32-row units 107; of 1024 rows 167,
 //     126 and 148.
 // A weight gradient's longest group is taken to hold 1.3 times the mean.
 GroupedPlan grouped_plan(int layout, int64_t E, int64_t R, int64_t N, int64_t K) {

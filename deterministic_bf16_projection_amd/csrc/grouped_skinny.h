@@ -15,7 +15,7 @@
 //    4), so that a load takes 256 contiguous bytes of four rows; a block holds
 //    the sum over its share of k, and the blocks are added across lanes once
 //    per unit.  Whole lines can be read past the caches: 256 rows of 64 groups,
-//    1024 x 4096, 93 us (5.8 TB/s); with 16x16x32 fragments, whose loads take
+//    1024 x 4096, 90 us (6.0 TB/s); with 16x16x32 fragments, whose loads take
 //    64 bytes of sixteen rows, 106, and 139 past the caches.
 //  forward, 32 rows by 32 columns: products of 16x16x32, lane l loading
 //    W[n0 + l % 16][k + 8 (l / 16) ..]; more rows share a weight's fragment.

@@ -17,7 +17,7 @@ struct RouteParams {
   int64_t ldl;
   int64_t T;
   int E, k, renorm;
-  int tokens_per_block;  // blocks of consecutive tokens, a multiple of kRouteRound
+  int tokens_per_block;  // blocks of consecutive tokens: 16, or a multiple of kRouteRound
   int blocks, hist_ld;
   int32_t* experts;      // [T, k]
   float* weights;        // [T, k]
@@ -397,9 +397,10 @@ __global__ void __launch_bounds__(256) route_dgrad_kernel(const float* logits, i
 // need not name each.  Positions come from device memory: one outside the
 // matrix is left out.
 //
-// Bound by memory: 16384 tokens, 8 slots each, 4096 columns of BF16 take 207 us
-// to dispatch (5.8 TB/s, what a copy reaches), 215 to combine (5.6) and 421 for
-// the gradients of that (5.4).
+// Bound by memory: 16384 tokens, 8 slots each, 4096 columns of BF16 take 247 us
+// to dispatch (4.9 TB/s), 223 to combine (5.4) and 444 for the gradients of that
+// (5.1) in a training pass, which finds the token side in no cache; called again
+// and again on the same rows 206, 212 and 421.
 struct RowsParams {
   const void* a;   // [T, H] of the token side
   const void* b;   // [R, H] sorted rows, read

@@ -321,15 +321,15 @@ int64_t dpg_plan_cache_capacity(void);
  *   stride_*: elements between groups' matrices, a multiple of 16 bytes (0: one
  *             weight for all groups).  Weight gradients must not overlap
  *             (stacked, or side by side in wider rows, as for the batched calls).
- * The plan depends on the sizes and the device's CU count alone, every sum runs
- * in a fixed order and nothing uses atomics: the bits are the same on every
+ * The plan depends on the sizes alone (it is made for 256 CUs whatever the
+ * device has), every sum runs in a fixed order and nothing uses atomics: the bits are the same on every
  * call and on every MI355X.  Where there are few output tiles the reduction is
  * split (each group's rows, for wgrad) and the parts are added in order from
  * the workspace: dpg_grouped_workspace_size bytes, 0 where nothing is split.
  * Row strides of x, dy and w below 2^22 elements and of outputs of more than one
  * row below 2^21, R, N, K below 2^31 - 512 and E below 2^24
- * (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an
- * empty reduction writes zeros.
+ * (DPG_ERR_UNSUPPORTED otherwise).  An empty output is a no-op; an empty
+ * reduction writes zeros.
  */
 size_t dpg_grouped_workspace_size(dpg_pass pass, int64_t E, int64_t R, int64_t N, int64_t K);
 /* Host-only description of a grouped call's plan (kernel, tile, K splits, the
@@ -394,7 +394,8 @@ dpg_status dpg_route_dgrad(const float* logits, int64_t ldl, const int32_t* expe
  * or not (R may exceed T * top_k); a row before it that none names stays as it
  * was.  T = 0 is a no-op: nothing is written.  Matrices follow the conventions at the top (16-byte rows); BF16 or FP32, one
  * type per call except that combine takes one for ys and one for y.  Positions
- * outside [0, R) are left out.
+ * outside [0, R) are left out.  R and T * top_k below 2^31, H and E at most 2^24
+ * (DPG_ERR_UNSUPPORTED beyond).
  */
 dpg_status dpg_dispatch(const void* x, int64_t ldx, const int32_t* positions, const int32_t* offsets, void* xs,
                         int64_t ldxs, dpg_dtype dtype, int64_t T, int64_t R, int64_t H, int64_t E, int64_t top_k,
