@@ -590,3 +590,8 @@ def dpg_wgrad_batched(dy, x, out=None, out_dtype=torch.bfloat16, weight_layout="
 # ----------------------------------------------------------- expert layers --
 from .experts import (ADAMW_BLOCK, Route, dpg_adamw, dpg_combine, dpg_combine_dgrad, dpg_dispatch,  # noqa: E402,F401
                       dpg_grouped_dgrad, dpg_grouped_forward, dpg_grouped_wgrad, dpg_route, dpg_route_dgrad)
+
+# ------------------------------------ between the projections of a block --
+from .blocks import (LayerNorm, LayerNormGrad, Recurrence, RecurrenceGrad, dpg_add_layer_norm,  # noqa: E402,F401
+                     dpg_add_layer_norm_dgrad, dpg_dropout, dpg_layer_norm, dpg_layer_norm_dgrad, dpg_recurrence,
+                     dpg_recurrence_dgrad)

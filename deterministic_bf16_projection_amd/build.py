@@ -17,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdpg.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("dpg_api.hip", "dpg_grouped.hip", "dpg_route.hip", "dpg_adamw.hip",
-                                                   "planner.cpp")]
+                                                   "dpg_norm.hip", "dpg_recurrence.hip", "planner.cpp")]
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"

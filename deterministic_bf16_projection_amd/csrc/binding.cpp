@@ -1,5 +1,5 @@
-// Python module _binding: the expert-layer entry points of include/dpg.h for
-// torch tensors.  It checks the arguments, allocates the outputs a caller does
+// Python module _binding: the entry points of include/dpg.h for expert layers and
+// for what stands between a block's projections, for torch tensors.  It checks the arguments, allocates the outputs a caller does
 // not give, and launches on the current stream of the tensors' device; no
 // arithmetic.  Compiled, because the same work through ctypes costs about 10 us
 // a call, and 90 us for an optimizer step over 48 tensors, where the kernels of
@@ -55,6 +55,7 @@ const char* dtype_text(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
+    case at::kLong: return "torch.int64";
     case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
@@ -539,6 +540,322 @@ PyObject* adamw(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// ------------------------------------- between the projections of a block --
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be a truth value");
+  }
+  return v != 0;
+}
+
+// p, seed and step of a dropout
+dpg_dropout_options dropout_of(PyObject* const* a, const Tensor& like) {
+  dpg_dropout_options o{};
+  o.p = number(a[0], "p");
+  o.seed = PyLong_AsUnsignedLongLongMask(a[1]);
+  if (o.seed == (uint64_t)-1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error("seed must be an integer");
+  }
+  if (a[2] != Py_None) {
+    const Tensor& step = packed(a[2], at::kLong, "step");
+    if (step.numel() != 1) value_error("step must hold one value");
+    same_device(like, step, "step");
+    o.step = data<int64_t>(step);
+  }
+  return o;
+}
+
+// FP32 [n], or null for None
+float* columns_of(PyObject* o, int64_t n, const Tensor& like, const char* name) {
+  if (o == Py_None) return nullptr;
+  const Tensor& t = floats(o, {n}, name);
+  same_device(like, t, name);
+  return data<float>(t);
+}
+
+void check_kind(const Tensor& t, at::ScalarType dtype, const char* name) {
+  if (t.scalar_type() != dtype) type_error(std::string(name) + " must be " + dtype_text(dtype));
+}
+
+// x, p, seed, step, residual, out, out_dtype
+PyObject* dropout(PyObject* const* a) {
+  const Tensor& x = rows_input(a[0], "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  const dpg_dropout_options o = dropout_of(a + 1, x);
+  at::ScalarType kind = x.scalar_type();
+  const void* r = nullptr;
+  int64_t ldr = 0;
+  if (a[4] != Py_None) {
+    const Tensor& residual = rows_input(a[4], "residual");
+    check_shape(residual, {T, H}, "residual");
+    same_device(x, residual, "residual");
+    kind = residual.scalar_type();
+    r = residual.data_ptr();
+    ldr = row_stride(residual, "residual");
+  }
+  const c10::DeviceGuard guard(x.device());
+  Tensor out = output(a[5], {T, H}, dtype_of(a[6], kind), x);
+  if (r) check_kind(out, kind, "out");
+  check_status(dpg_dropout(x.data_ptr(), row_stride(x, "x"), code_of(x.scalar_type()), T > 0 && H > 0 ? r : nullptr, ldr,
+                           out.data_ptr(), row_stride(out, "out"), code_of(out.scalar_type()), T, H, &o, stream_of(x)),
+               "dpg_dropout");
+  written(a[5], out);
+  return wrap(std::move(out));
+}
+
+// x, weight, bias, eps, out, out_dtype
+PyObject* layer_norm(PyObject* const* a) {
+  const Tensor& x = rows_input(a[0], "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  const float *w = columns_of(a[1], H, x, "weight"), *b = columns_of(a[2], H, x, "bias");
+  const double eps = number(a[3], "eps");
+  const c10::DeviceGuard guard(x.device());
+  Tensor out = output(a[4], {T, H}, dtype_of(a[5], x.scalar_type()), x);
+  Block block(2 * Block::padded(4 * T), x);
+  Tensor mean = block.part({T}, at::kFloat), rstd = block.part({T}, at::kFloat);
+  check_status(dpg_layer_norm(x.data_ptr(), row_stride(x, "x"), code_of(x.scalar_type()), w, b, out.data_ptr(),
+                              row_stride(out, "out"), code_of(out.scalar_type()), data<float>(mean), data<float>(rstd),
+                              T, H, eps, stream_of(x)),
+               "dpg_layer_norm");
+  written(a[4], out);
+  return Py_BuildValue("(NNN)", wrap(std::move(out)), wrap(std::move(mean)), wrap(std::move(rstd)));
+}
+
+// x, residual, weight, bias, eps, p, seed, step, out, sum, out_dtype
+PyObject* add_layer_norm(PyObject* const* a) {
+  const Tensor& x = rows_input(a[0], "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  const Tensor& residual = rows_input(a[1], "residual");
+  check_shape(residual, {T, H}, "residual");
+  same_device(x, residual, "residual");
+  const float *w = columns_of(a[2], H, x, "weight"), *b = columns_of(a[3], H, x, "bias");
+  const double eps = number(a[4], "eps");
+  const dpg_dropout_options o = dropout_of(a + 5, x);
+  const c10::DeviceGuard guard(x.device());
+  Tensor out = output(a[8], {T, H}, dtype_of(a[10], x.scalar_type()), x);
+  Tensor sum = output(a[9], {T, H}, residual.scalar_type(), x);
+  check_kind(sum, residual.scalar_type(), "sum");
+  Block block(2 * Block::padded(4 * T), x);
+  Tensor mean = block.part({T}, at::kFloat), rstd = block.part({T}, at::kFloat);
+  check_status(dpg_add_layer_norm(x.data_ptr(), row_stride(x, "x"), code_of(x.scalar_type()), residual.data_ptr(),
+                                  row_stride(residual, "residual"), sum.data_ptr(), row_stride(sum, "sum"),
+                                  code_of(sum.scalar_type()), w, b, out.data_ptr(), row_stride(out, "out"),
+                                  code_of(out.scalar_type()), data<float>(mean), data<float>(rstd), T, H, eps, &o,
+                                  stream_of(x)),
+               "dpg_add_layer_norm");
+  written(a[8], out);
+  written(a[9], sum);
+  return Py_BuildValue("(NNNN)", wrap(std::move(out)), wrap(std::move(mean)), wrap(std::move(rstd)),
+                       wrap(std::move(sum)));
+}
+
+// The gradients of weight and bias, and the workspace that their sums go through.
+struct WeightGrads {
+  Tensor dweight, dbias, workspace;
+  WeightGrads(bool wanted, int64_t T, int64_t H, PyObject* given, const Tensor& like) {
+    if (!wanted) return;
+    Block block(2 * Block::padded(4 * H), like);
+    dweight = block.part({H}, at::kFloat);
+    dbias = block.part({H}, at::kFloat);
+    const size_t need = dpg_layer_norm_workspace_size(T, H);
+    if (need != (size_t)-1) workspace = workspace_of(given, need, like);
+  }
+  static float* at(const Tensor& t) { return t.defined() ? data<float>(t) : nullptr; }
+  static PyObject* object(Tensor& t) {
+    if (t.defined()) return wrap(std::move(t));
+    Py_RETURN_NONE;
+  }
+};
+
+// dy, x, mean, rstd, weight, weight_grads, workspace
+PyObject* layer_norm_dgrad(PyObject* const* a) {
+  const Tensor& dy = rows_input(a[0], "dy");
+  const int64_t T = dy.size(0), H = dy.size(1);
+  const Tensor& x = rows_input(a[1], "x");
+  check_shape(x, {T, H}, "x");
+  same_device(dy, x, "x");
+  const Tensor &mean = floats(a[2], {T}, "mean"), &rstd = floats(a[3], {T}, "rstd");
+  same_device(dy, mean, "mean");
+  same_device(dy, rstd, "rstd");
+  const float* w = columns_of(a[4], H, dy, "weight");
+  const bool wanted = truth(a[5], "weight_grads");
+  const c10::DeviceGuard guard(dy.device());
+  Tensor dx = fresh({T, H}, x.scalar_type(), dy);
+  WeightGrads g(wanted, T, H, a[6], dy);
+  check_status(dpg_layer_norm_dgrad(dy.data_ptr(), row_stride(dy, "dy"), code_of(dy.scalar_type()), x.data_ptr(),
+                                    row_stride(x, "x"), code_of(x.scalar_type()), data<float>(mean), data<float>(rstd),
+                                    w, dx.data_ptr(), row_stride(dx, "dx"), g.at(g.dweight), g.at(g.dbias), T, H,
+                                    workspace_data(g.workspace), workspace_bytes(g.workspace), stream_of(dy)),
+               "dpg_layer_norm_dgrad");
+  return Py_BuildValue("(NNN)", wrap(std::move(dx)), g.object(g.dweight), g.object(g.dbias));
+}
+
+// dy, sum, mean, rstd, weight, dsum, p, seed, step, x_dtype, weight_grads, workspace
+PyObject* add_layer_norm_dgrad(PyObject* const* a) {
+  const Tensor& dy = rows_input(a[0], "dy");
+  const int64_t T = dy.size(0), H = dy.size(1);
+  const Tensor& sum = rows_input(a[1], "sum");
+  check_shape(sum, {T, H}, "sum");
+  same_device(dy, sum, "sum");
+  const Tensor &mean = floats(a[2], {T}, "mean"), &rstd = floats(a[3], {T}, "rstd");
+  same_device(dy, mean, "mean");
+  same_device(dy, rstd, "rstd");
+  const float* w = columns_of(a[4], H, dy, "weight");
+  const void* more = nullptr;
+  int64_t ldm = 0;
+  if (a[5] != Py_None) {
+    const Tensor& dsum = rows_input(a[5], "dsum");
+    check_shape(dsum, {T, H}, "dsum");
+    check_kind(dsum, sum.scalar_type(), "dsum");
+    same_device(dy, dsum, "dsum");
+    more = T > 0 && H > 0 ? dsum.data_ptr() : nullptr;
+    ldm = row_stride(dsum, "dsum");
+  }
+  const dpg_dropout_options o = dropout_of(a + 6, dy);
+  const at::ScalarType kind = dtype_of(a[9], dy.scalar_type());
+  const bool wanted = truth(a[10], "weight_grads");
+  const c10::DeviceGuard guard(dy.device());
+  code_of(kind);
+  Tensor dx = fresh({T, H}, kind, dy), dres = fresh({T, H}, sum.scalar_type(), dy);
+  WeightGrads g(wanted, T, H, a[11], dy);
+  check_status(dpg_add_layer_norm_dgrad(dy.data_ptr(), row_stride(dy, "dy"), code_of(dy.scalar_type()), sum.data_ptr(),
+                                        row_stride(sum, "sum"), code_of(sum.scalar_type()), data<float>(mean),
+                                        data<float>(rstd), w, more, ldm, dx.data_ptr(), row_stride(dx, "dx"),
+                                        code_of(kind), dres.data_ptr(), row_stride(dres, "dresidual"),
+                                        g.at(g.dweight), g.at(g.dbias), T, H, &o, workspace_data(g.workspace),
+                                        workspace_bytes(g.workspace), stream_of(dy)),
+               "dpg_add_layer_norm_dgrad");
+  return Py_BuildValue("(NNNN)", wrap(std::move(dx)), wrap(std::move(dres)), g.object(g.dweight), g.object(g.dbias));
+}
+
+// Sequences of a recurrence: x is [B, T, D], or [R, D] with offsets [S + 1].
+struct Sequences {
+  int64_t S, R, D;
+  const int32_t* offsets;
+  at::ScalarType kind;
+  Sequences(const Tensor& x, PyObject* off) : offsets(nullptr), kind(x.scalar_type()) {
+    if (off == Py_None) {
+      if (x.dim() != 3) value_error("x must be [B, T, D], or [R, D] with offsets");
+      S = x.size(0);
+      R = S * x.size(1);
+      D = x.size(2);
+    } else {
+      if (x.dim() != 2) value_error("x must be [R, D] with offsets");
+      const Tensor& t = offsets_of(off, -1);
+      same_device(x, t, "offsets");
+      S = t.size(0) - 1;
+      R = x.size(0);
+      D = x.size(1);
+      offsets = data<int32_t>(t);
+    }
+  }
+};
+
+const Tensor& sequence_input(PyObject* o, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+    type_error(std::string(name) + " must be torch.bfloat16 or torch.float32");
+  if (!t.is_cuda()) value_error(std::string(name) + " must be a device tensor");
+  return t;
+}
+const Tensor& sequence_like(PyObject* o, const Tensor& x, const char* name) {
+  const Tensor& t = sequence_input(o, name);
+  check_kind(t, x.scalar_type(), name);
+  check_shape(t, x.sizes(), name);
+  same_device(x, t, name);
+  return t;
+}
+
+// One stride between all rows, those of one sequence and of the next.
+int64_t sequence_stride(const Tensor& t, const char* name) {
+  if (t.dim() == 2) return row_stride(t, name);
+  const int64_t b = t.size(0), n = t.size(1), d = t.size(2), wide = std::max<int64_t>(8, (d + 7) / 8 * 8);
+  if (t.numel() == 0) return wide;
+  if (d > 1 && t.stride(2) != 1) value_error(std::string(name) + ": the last dimension must be contiguous");
+  if (n == 1) return b > 1 ? t.stride(0) : wide;
+  if (b > 1 && t.stride(0) != n * t.stride(1))
+    value_error(std::string(name) + ": sequences must follow each other at the stride of their rows");
+  return t.stride(1);
+}
+
+// x, gate, offsets, state, coupled, carries, out, state_out, workspace
+PyObject* recurrence(PyObject* const* a) {
+  const Tensor& x = sequence_input(a[0], "x");
+  const Sequences q(x, a[2]);
+  const Tensor& gate = sequence_like(a[1], x, "gate");
+  const float* state = nullptr;
+  if (a[3] != Py_None) {
+    const Tensor& t = floats(a[3], {q.S, q.D}, "state");
+    same_device(x, t, "state");
+    state = data<float>(t);
+  }
+  const bool coupled = truth(a[4], "coupled"), keep = truth(a[5], "carries");
+  const c10::DeviceGuard guard(x.device());
+  Tensor out = output(a[6], x.sizes(), q.kind, x);
+  check_kind(out, q.kind, "out");
+  Tensor last;
+  if (a[7] == Py_None) {
+    last = fresh({q.S, q.D}, at::kFloat, x);
+  } else {
+    last = floats(a[7], {q.S, q.D}, "state_out");
+    same_device(x, last, "state_out");
+  }
+  const int packed_rows = q.offsets != nullptr;
+  const dpg_dtype kind = code_of(q.kind);
+  const size_t need = dpg_recurrence_workspace_size(q.S, q.R, q.D, kind, packed_rows);
+  const size_t carry = dpg_recurrence_carries_size(q.S, q.R, q.D, kind, packed_rows);
+  if (need == (size_t)-1) throw Status{DPG_ERR_UNSUPPORTED, "dpg_recurrence"};
+  const Tensor ws = workspace_of(a[8], need, x);
+  Tensor carries;
+  if (keep) carries = fresh({(int64_t)(carry / 4)}, at::kFloat, x);
+  check_status(dpg_recurrence(gate.data_ptr(), sequence_stride(gate, "gate"), x.data_ptr(), sequence_stride(x, "x"),
+                              out.data_ptr(), sequence_stride(out, "out"), kind, state, data<float>(last),
+                              carries.defined() ? data<float>(carries) : nullptr, q.offsets, q.S, q.R, q.D, coupled,
+                              workspace_data(ws), workspace_bytes(ws), stream_of(x)),
+               "dpg_recurrence");
+  written(a[6], out);
+  written(a[7], last);
+  return Py_BuildValue("(NNN)", wrap(std::move(out)), wrap(std::move(last)), WeightGrads::object(carries));
+}
+
+// dh, gate, x, carries, offsets, state, dstate, coupled, workspace
+PyObject* recurrence_dgrad(PyObject* const* a) {
+  const Tensor& x = sequence_input(a[2], "x");
+  const Sequences q(x, a[4]);
+  const Tensor &gate = sequence_like(a[1], x, "gate"), &dh = sequence_like(a[0], x, "dh");
+  const int packed_rows = q.offsets != nullptr;
+  const dpg_dtype kind = code_of(q.kind);
+  const size_t need = dpg_recurrence_workspace_size(q.S, q.R, q.D, kind, packed_rows);
+  const size_t carry = dpg_recurrence_carries_size(q.S, q.R, q.D, kind, packed_rows);
+  if (need == (size_t)-1) throw Status{DPG_ERR_UNSUPPORTED, "dpg_recurrence_dgrad"};
+  const Tensor& carries = floats(a[3], {(int64_t)(carry / 4)}, "carries");
+  same_device(x, carries, "carries");
+  const float* states[2] = {nullptr, nullptr};
+  const char* const names[2] = {"state", "dstate"};
+  for (int i = 0; i < 2; ++i) {
+    if (a[5 + i] == Py_None) continue;
+    const Tensor& t = floats(a[5 + i], {q.S, q.D}, names[i]);
+    same_device(x, t, names[i]);
+    states[i] = data<float>(t);
+  }
+  const bool coupled = truth(a[7], "coupled");
+  const c10::DeviceGuard guard(x.device());
+  const Tensor ws = workspace_of(a[8], need, x);
+  Tensor dgate = fresh(x.sizes(), q.kind, x), dx = fresh(x.sizes(), q.kind, x), first;
+  if (states[0]) first = fresh({q.S, q.D}, at::kFloat, x);
+  check_status(dpg_recurrence_dgrad(dh.data_ptr(), sequence_stride(dh, "dh"), gate.data_ptr(),
+                                    sequence_stride(gate, "gate"), x.data_ptr(), sequence_stride(x, "x"),
+                                    data<float>(carries), states[0], states[1], dgate.data_ptr(),
+                                    sequence_stride(dgate, "dgate"), dx.data_ptr(), sequence_stride(dx, "dx"),
+                                    first.defined() ? data<float>(first) : nullptr, kind, q.offsets, q.S, q.R, q.D,
+                                    coupled, workspace_data(ws), workspace_bytes(ws), stream_of(x)),
+               "dpg_recurrence_dgrad");
+  return Py_BuildValue("(NNN)", wrap(std::move(dgate)), wrap(std::move(dx)), WeightGrads::object(first));
+}
+
 // Entry with a fixed number of positional arguments; C++ exceptions end here.
 template <PyObject* (*FN)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -581,6 +898,13 @@ PyMethodDef g_methods[] = {ENTRY(grouped_forward, 6),
                            ENTRY(combine, 6),
                            ENTRY(combine_dgrad, 5),
                            ENTRY(adamw, 15),
+                           ENTRY(dropout, 7),
+                           ENTRY(layer_norm, 6),
+                           ENTRY(add_layer_norm, 11),
+                           ENTRY(layer_norm_dgrad, 7),
+                           ENTRY(add_layer_norm_dgrad, 12),
+                           ENTRY(recurrence, 9),
+                           ENTRY(recurrence_dgrad, 9),
                            {"set_error", &set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 #undef ENTRY

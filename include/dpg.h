@@ -455,6 +455,124 @@ typedef struct {
 dpg_status dpg_adamw(const dpg_adamw_tensor* tensors, int64_t count, const dpg_adamw_options* options,
                      hipStream_t stream);
 
+/*
+ * Dropout from a counter-based generator (Philox4x32, ten rounds): the mask is a
+ * function of seed, step and an element's place in the [T, H] matrix (whatever
+ * the strides), so it is never stored, and the same options give it again.
+ *   p    : in [0, 1], taken to the nearest multiple of 2^-16; the elements kept
+ *          are multiplied by 1 / (1 - p), and what is left out counts as 0
+ *          whatever it holds.  p = 1 leaves nothing.
+ *   seed : any 64 bits
+ *   step : int64 on the DEVICE, 8-byte aligned, or NULL for 0.  A captured call
+ *          reads it at each replay: a caller that counts it up on the device
+ *          gets another mask each time.
+ * Element 8 g + j of the matrix, row after row, takes 16 of the 128 bits of
+ * counter (g, step) under the key `seed`: half j % 2 (low first) of word j / 2;
+ * it is left out where they are below 65536 p.
+ *
+ *   y = keep x / (1 - p) [+ residual]
+ * residual, of y's type, may be NULL.  y may be x or residual itself (same type
+ * and strides).  The gradient by x is the same call on dy without a residual.
+ * T and H below 2^31 (DPG_ERR_UNSUPPORTED beyond).
+ */
+typedef struct {
+  double p;
+  uint64_t seed;
+  const int64_t* step;
+} dpg_dropout_options;
+dpg_status dpg_dropout(const void* x, int64_t ldx, dpg_dtype x_dtype, const void* residual, int64_t ldr, void* y,
+                       int64_t ldy, dpg_dtype y_dtype, int64_t T, int64_t H, const dpg_dropout_options* options,
+                       hipStream_t stream);
+
+/*
+ * Layer norm over the H columns of each row, FP32 inside:
+ *   mean = sum v / H                 rstd = (sum (v - mean)^2 / H + eps)^-1/2
+ *   n = (v - mean) rstd              y = n weight + bias
+ * of v = x, or (dpg_add_layer_norm) of the sum that a residual block goes on
+ * with, v = residual + keep x / (1 - p), which is written to `sum` (of
+ * residual's type; it may be residual itself) and normalised as it was before
+ * that rounding.
+ *   weight, bias : FP32 [H], 16-byte aligned; NULL: ones, zeros
+ *   mean, rstd   : FP32 [T], outputs, which the gradient reads
+ *   options      : NULL: no dropout
+ * Gradients, with u = dy weight:
+ *   dv = rstd (u - sum u / H - n sum(u n) / H) + dsum
+ *   dweight = sum over the rows of dy n          dbias = sum over the rows of dy
+ * dx = dv alone; of a sum, dresidual = dv (of sum's type) and dx = keep dv / (1 -
+ * p) (of a type of its own), with the forward call's options and the matrix
+ * that it wrote to `sum`.  dsum (of sum's type), the gradient that reaches the
+ * sum from elsewhere, may be NULL; dresidual may be dsum itself.  dweight and
+ * dbias are FP32 [H], either may be NULL; T = 0 writes zeros to them.  Their
+ * sums run in a fixed order through dpg_layer_norm_workspace_size bytes, 16-byte
+ * aligned (not needed where both are NULL).  T below 2^31, H at most 16384
+ * (DPG_ERR_UNSUPPORTED beyond).
+ */
+dpg_status dpg_layer_norm(const void* x, int64_t ldx, dpg_dtype x_dtype, const float* weight, const float* bias,
+                          void* y, int64_t ldy, dpg_dtype y_dtype, float* mean, float* rstd, int64_t T, int64_t H,
+                          double eps, hipStream_t stream);
+dpg_status dpg_add_layer_norm(const void* x, int64_t ldx, dpg_dtype x_dtype, const void* residual, int64_t ldr,
+                              void* sum, int64_t lds, dpg_dtype sum_dtype, const float* weight, const float* bias,
+                              void* y, int64_t ldy, dpg_dtype y_dtype, float* mean, float* rstd, int64_t T, int64_t H,
+                              double eps, const dpg_dropout_options* options, hipStream_t stream);
+size_t dpg_layer_norm_workspace_size(int64_t T, int64_t H);
+dpg_status dpg_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_dtype, const void* x, int64_t ldx,
+                                dpg_dtype x_dtype, const float* mean, const float* rstd, const float* weight, void* dx,
+                                int64_t lddx, float* dweight, float* dbias, int64_t T, int64_t H, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_dtype, const void* sum, int64_t lds,
+                                    dpg_dtype sum_dtype, const float* mean, const float* rstd, const float* weight,
+                                    const void* dsum, int64_t lddsum, void* dx, int64_t lddx, dpg_dtype dx_dtype,
+                                    void* dresidual, int64_t lddr, float* dweight, float* dbias, int64_t T, int64_t H,
+                                    const dpg_dropout_options* options, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/*
+ * A gated linear recurrence over sequences, channel by channel in FP32:
+ *   f = 1 / (1 + e^-gate)     w = 1 - f if `coupled`, else 1
+ *   h[t] = f[t] h[t - 1] + w[t] x[t]
+ * gate, x, h : [R, D], BF16 or FP32, one type per call; h may be x itself
+ * offsets    : NULL: S sequences of R / S rows each, one after the other (S has
+ *              to divide R; one row each is a generation step).  Else int32
+ *              [S + 1] on the DEVICE, ascending, offsets[0] taken as 0: sequence
+ *              s has the rows [offsets[s], offsets[s + 1]).  Sequences may be
+ *              empty.  Rows from offsets[S] on are not read, and their rows in
+ *              the outputs are zeros.  Offsets outside [0, R] or descending give
+ *              unspecified values, never an access outside the operands.
+ * state      : FP32 [S, D], h before each sequence's first row; NULL: zeros
+ * state_out  : FP32 [S, D], h after its last row (an empty one's is its state);
+ *              NULL: not wanted; may be `state` itself
+ * carries    : FP32, dpg_recurrence_carries_size bytes, for the gradient; NULL:
+ *              not wanted
+ * A weight that is exactly 0 leaves its term out whatever the term is, so a
+ * gate of -infinity (any below about -88 counts as one) forgets the state, and
+ * one of +infinity with `coupled` passes over the input.
+ *
+ * Gradient, from dh [R, D] of h and dstate [S, D] (or NULL: zeros) of state_out,
+ * with the forward call's inputs and what it wrote to `carries`:
+ *   r[t] = dh[t] + f[t + 1] r[t + 1]      (dstate behind a sequence's last row)
+ *   dx[t] = w[t] r[t]
+ *   dgate[t] = f[t] (1 - f[t]) r[t] (h[t - 1] - x[t] if `coupled`, else h[t - 1])
+ * and into dstate_out (or NULL), not dstate itself, f r of each first row (an
+ * empty sequence's is its dstate).
+ *
+ * The states between carries are recomputed in FP32.  Sums run in a fixed order
+ * that depends on the sizes alone.  Workspace: dpg_recurrence_workspace_size
+ * bytes, 16-byte aligned; packed = whether offsets are given.  State matrices
+ * and carries are 16-byte aligned.  R at most 2^30, S and D at most 2^24
+ * (DPG_ERR_UNSUPPORTED beyond, and for launches of more than 2^23 workgroups).
+ */
+size_t dpg_recurrence_workspace_size(int64_t S, int64_t R, int64_t D, dpg_dtype dtype, int packed);
+size_t dpg_recurrence_carries_size(int64_t S, int64_t R, int64_t D, dpg_dtype dtype, int packed);
+dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t ldx, void* h, int64_t ldh,
+                          dpg_dtype dtype, const float* state, float* state_out, float* carries,
+                          const int32_t* offsets, int64_t S, int64_t R, int64_t D, int coupled, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, int64_t ldg, const void* x, int64_t ldx,
+                                const float* carries, const float* state, const float* dstate, void* dgate,
+                                int64_t lddg, void* dx, int64_t lddx, float* dstate_out, dpg_dtype dtype,
+                                const int32_t* offsets, int64_t S, int64_t R, int64_t D, int coupled, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
 /* Static text for a status code ("unknown status" for other values); the
  * error classes follow the validation rules above. */
 const char* dpg_status_string(dpg_status status);
