@@ -15,6 +15,13 @@ the expert layer's entry points; an expert layer is
     h = grouped_projection(dispatch(x, r), w_experts, r.offsets)
     y = combine(h, r)
 
+``layer_norm``, ``add_layer_norm``, ``dropout`` and ``recurrence`` are what stands
+between the projections of a residual block:
+
+    h, stream = add_layer_norm(y, stream, w_norm, b_norm, p=p, seed=seed, step=step)
+    m, state = recurrence(projection(h, w_gate), projection(h, w_in))
+    y = projection(m, w_out)
+
 Their gradients have no gradients: differentiating twice raises.
 
 Argument marshalling only, as in the rest of the package: every product runs
@@ -29,6 +36,8 @@ from torch.autograd.function import once_differentiable
 
 from . import (Route, dpg_combine, dpg_combine_dgrad, dpg_dispatch, dpg_grouped_dgrad, dpg_grouped_forward,
                dpg_grouped_wgrad, dpg_route, dpg_route_dgrad)
+from . import (dpg_add_layer_norm, dpg_add_layer_norm_dgrad, dpg_dropout, dpg_layer_norm, dpg_layer_norm_dgrad,
+               dpg_recurrence, dpg_recurrence_dgrad)
 from . import (dpg_dgrad, dpg_forward, dpg_router_dgrad, dpg_router_forward, dpg_router_wgrad, dpg_wgrad,
                workspace_size, PASS_FORWARD, PASS_DGRAD, PASS_WGRAD)
 
@@ -230,6 +239,130 @@ def combine(ys, r):
     """y[t] = sum_j weights[t, j] ys[positions[t, j]], as [..., H] with the leading
     dimensions of the route r; differentiable in ys and in the route's weights."""
     return _Combine.apply(ys, r.weights, r.positions, r.offsets)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, out_dtype):
+        matrix = _matrix(x)
+        n = dpg_layer_norm(matrix, weight, bias, eps=eps, out_dtype=out_dtype)
+        ctx.save_for_backward(matrix, weight, n.mean, n.rstd)
+        ctx.shape = x.shape
+        return n.y.view(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        matrix, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        d = dpg_layer_norm_dgrad(_rows(dy), matrix, mean, rstd, weight, weight_grads=need[1] or need[2])
+        return (d.dx.view(ctx.shape) if need[0] else None, d.dweight if need[1] else None,
+                d.dbias if need[2] else None, None, None)
+
+
+class _AddLayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, p, seed, step, out_dtype):
+        n = dpg_add_layer_norm(_matrix(x), _matrix(residual), weight, bias, eps=eps, p=p, seed=seed, step=step,
+                               out_dtype=out_dtype)
+        total = n.sum.view(x.shape)
+        # the step is saved too: counting it up before the backward pass, which
+        # needs the same mask, is an error that its version shows
+        ctx.save_for_backward(total, weight, n.mean, n.rstd, step)
+        ctx.drop, ctx.x_dtype = (p, seed), x.dtype
+        ctx.set_materialize_grads(False)
+        return n.y.view(x.shape), total
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum):
+        total, weight, mean, rstd, step = ctx.saved_tensors
+        need, (p, seed), shape = ctx.needs_input_grad, ctx.drop, total.shape
+        if dy is None and dsum is None:
+            return (None,) * 9
+        if dy is None:
+            # nothing came through the norm
+            dx = dpg_dropout(_rows(dsum), p, seed, step=step, out_dtype=ctx.x_dtype).view(shape) if need[0] else None
+            return (dx, dsum if need[1] else None) + (None,) * 7
+        d = dpg_add_layer_norm_dgrad(_rows(dy), _rows(total), mean, rstd, weight,
+                                     dsum=None if dsum is None else _rows(dsum), p=p, seed=seed, step=step,
+                                     x_dtype=ctx.x_dtype, weight_grads=need[2] or need[3])
+        return (d.dx.view(shape) if need[0] else None, d.dresidual.view(shape) if need[1] else None,
+                d.dweight if need[2] else None, d.dbias if need[3] else None) + (None,) * 5
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, step, residual):
+        ctx.save_for_backward(step)
+        ctx.drop, ctx.x_dtype = (p, seed), x.dtype
+        y = dpg_dropout(_matrix(x), p, seed, step=step, residual=None if residual is None else _matrix(residual))
+        return y.view(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (step,) = ctx.saved_tensors
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = dpg_dropout(_rows(dy), *ctx.drop, step=step, out_dtype=ctx.x_dtype).view(dy.shape)
+        return dx, None, None, None, dy if ctx.needs_input_grad[4] else None
+
+
+def _sequences(t):
+    """t itself where all its rows are one stride apart, else a copy."""
+    if t.dim() == 2:
+        return _matrix(t)
+    b, n, d = t.shape
+    last = d <= 1 or t.stride(2) == 1
+    even = n <= 1 or (t.stride(1) >= d and (b <= 1 or t.stride(0) == n * t.stride(1)))
+    return t if last and even and (n > 1 or b <= 1 or t.stride(0) >= d) else t.contiguous()
+
+
+class _Recurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, x, offsets, state, coupled):
+        gate, x = _sequences(gate), _sequences(x)
+        r = dpg_recurrence(gate, x, offsets=offsets, state=state, coupled=coupled, carries=any(ctx.needs_input_grad))
+        ctx.save_for_backward(gate, x, r.carries, offsets, state)
+        ctx.coupled = coupled
+        ctx.set_materialize_grads(False)
+        return r.h, r.state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dstate):
+        gate, x, carries, offsets, state = ctx.saved_tensors
+        if dh is None and dstate is None:
+            return (None,) * 5
+        dh = torch.zeros_like(x) if dh is None else _sequences(dh)
+        d = dpg_recurrence_dgrad(dh, gate, x, carries, offsets=offsets, state=state,
+                                 dstate=None if dstate is None else dstate.contiguous(), coupled=ctx.coupled)
+        return d.dgate, d.dx, None, d.dstate, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None):
+    """dpg_layer_norm over the last dimension of x [..., H]; differentiable in x
+    (gradient of x's type), weight and bias (FP32)."""
+    return _LayerNorm.apply(x, weight, bias, eps, out_dtype)
+
+
+def add_layer_norm(x, residual, weight=None, bias=None, eps=1e-5, p=0.0, seed=0, step=None, out_dtype=None):
+    """(y, sum) of dpg_add_layer_norm on [..., H]: the residual stream that goes on
+    and its norm; differentiable in x, residual, weight and bias.  Pass p=0 in
+    evaluation."""
+    return _AddLayerNorm.apply(x, residual, weight, bias, eps, p, seed, step, out_dtype)
+
+
+def dropout(x, p, seed, step=None, residual=None):
+    """dpg_dropout on [..., H]; differentiable in x and residual."""
+    return _Dropout.apply(x, p, seed, step, residual)
+
+
+def recurrence(gate, x, offsets=None, state=None, coupled=True):
+    """(h, state) of dpg_recurrence on [B, T, D], or [R, D] with offsets;
+    differentiable in gate, x and state."""
+    return _Recurrence.apply(gate, x, offsets, state, bool(coupled))
 
 
 class CheckpointedStep:
