@@ -28,8 +28,8 @@ struct RecPlan {
 };
 
 // S sequences in R rows of D channels; R > 0.
-dpg_status rec_plan(int64_t S, int64_t R, int64_t D, int dtype, bool packed, RecPlan& g) {
-  const int64_t tile = rec_tile_rows(dtype == DPG_BF16);
+dpg_status rec_plan(int64_t S, int64_t R, int64_t D, bool packed, RecPlan& g) {
+  const int64_t tile = kRecTileRows;
   g = RecPlan{};
   if (packed) {
     g.axis_rows = R;
@@ -47,7 +47,7 @@ dpg_status rec_plan(int64_t S, int64_t R, int64_t D, int dtype, bool packed, Rec
     g.spans = std::min((kRecFull + have - 1) / have, g.tiles / 2);
   g.span_tiles = (g.tiles + g.spans - 1) / g.spans;
   g.spans = (g.tiles + g.span_tiles - 1) / g.span_tiles;
-  if (g.axes * g.spans * g.blocks >= (1ll << 23)) return DPG_ERR_UNSUPPORTED;
+  if (g.axes * g.spans * g.blocks >= (1ll << 22)) return DPG_ERR_UNSUPPORTED;
   g.seq_bytes = packed ? padded((size_t)R * sizeof(int32_t)) : 0;
   if (g.spans > 1) {
     g.summary_bytes = padded((size_t)(g.axes * g.spans * 2 * D) * sizeof(float));
@@ -120,14 +120,14 @@ size_t dpg_recurrence_workspace_size(int64_t S, int64_t R, int64_t D, dpg_dtype 
   if (check_sizes(S, R, D, (int)dtype, packed != 0) != DPG_OK) return (size_t)-1;
   if (R == 0 || D == 0) return 0;
   RecPlan g;
-  return rec_plan(S, R, D, (int)dtype, packed != 0, g) == DPG_OK ? g.workspace() : (size_t)-1;
+  return rec_plan(S, R, D, packed != 0, g) == DPG_OK ? g.workspace() : (size_t)-1;
 }
 
 size_t dpg_recurrence_carries_size(int64_t S, int64_t R, int64_t D, dpg_dtype dtype, int packed) {
   if (check_sizes(S, R, D, (int)dtype, packed != 0) != DPG_OK) return (size_t)-1;
   if (R == 0 || D == 0) return 0;
   RecPlan g;
-  return rec_plan(S, R, D, (int)dtype, packed != 0, g) == DPG_OK ? g.carry_bytes : (size_t)-1;
+  return rec_plan(S, R, D, packed != 0, g) == DPG_OK ? g.carry_bytes : (size_t)-1;
 }
 
 dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t ldx, void* h, int64_t ldh,
@@ -146,7 +146,7 @@ dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t 
   if (D == 0) return DPG_OK;
   if (R == 0) return state_out == state ? DPG_OK : run_rows(nullptr, S, 0, nullptr, state, state_out, D, stream);
   RecPlan g;
-  if ((st = rec_plan(S, R, D, (int)dtype, packed, g)) != DPG_OK) return st;
+  if ((st = rec_plan(S, R, D, packed, g)) != DPG_OK) return st;
   if (g.workspace() > 0 && (!workspace || workspace_bytes < g.workspace() || !aligned16(workspace)))
     return DPG_ERR_WORKSPACE;
   RecParams p{};
@@ -172,10 +172,10 @@ dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t 
       if (st != DPG_OK) return st;
       p.state = (const float*)to;
     }
-    st = launch(forward_span_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, 256, 0, args, stream);
+    st = launch(forward_span_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
     if (st != DPG_OK) return st;
   }
-  return launch(forward_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, 256, 0, args, stream);
+  return launch(forward_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
 }
 
 dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, int64_t ldg, const void* x, int64_t ldx,
@@ -200,7 +200,7 @@ dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, 
   if (R == 0) return run_rows(nullptr, S, 0, nullptr, dstate, dstate_out, D, stream);
   if (!carries) return DPG_ERR_INVALID_ARG;
   RecPlan g;
-  if ((st = rec_plan(S, R, D, (int)dtype, packed, g)) != DPG_OK) return st;
+  if ((st = rec_plan(S, R, D, packed, g)) != DPG_OK) return st;
   if (g.workspace() > 0 && (!workspace || workspace_bytes < g.workspace() || !aligned16(workspace)))
     return DPG_ERR_WORKSPACE;
   RecParams p{};
@@ -218,10 +218,10 @@ dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, 
     return st;
   void* args[] = {&p};
   if (g.spans > 1) {
-    st = launch(dgrad_span_fn(bf16), g.axes * g.spans * g.blocks, 256, 0, args, stream);
+    st = launch(dgrad_span_fn(bf16), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
     if (st != DPG_OK) return st;
   }
-  return launch(dgrad_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, 256, 0, args, stream);
+  return launch(dgrad_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
 }
 
 }  // extern "C"
