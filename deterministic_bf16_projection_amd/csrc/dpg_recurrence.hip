@@ -13,12 +13,15 @@ namespace {
 
 constexpr int64_t kRecMaxRows = 1 << 30;  // places behind the last row are counted in 32 bits too
 constexpr int64_t kRecMaxOther = 1 << 24;  // sequences, channels
-// Workgroups that fill the device: two to each of 256 CUs.
-constexpr int64_t kRecFull = 512;
+// Workgroups that fill the device: one to each of 256 CUs.
+constexpr int64_t kRecFull = 256;
 
 bool row_type(int dtype) { return dtype == DPG_BF16 || dtype == DPG_F32; }
 Rows8 rows8(const void* data, int64_t ld) { return Rows8{const_cast<void*>(data), ld}; }
 size_t padded(size_t bytes) { return (bytes + 15) & ~(size_t)15; }
+
+// Matrices that do not fit the XCDs' 32 MB of L2 go past it.
+bool past_caches(int64_t R, int64_t D, int elt) { return R * D >= (int64_t)(32 << 20) / elt; }
 
 struct RecPlan {
   int64_t length;                 // of a sequence, 0 where they are packed
@@ -53,7 +56,7 @@ dpg_status rec_plan(int64_t S, int64_t R, int64_t D, bool packed, RecPlan& g) {
     g.summary_bytes = padded((size_t)(g.axes * g.spans * 2 * D) * sizeof(float));
     g.copy_bytes = padded((size_t)(S * D) * sizeof(float));
   }
-  g.carry_bytes = (size_t)(g.axes * g.tiles * D) * sizeof(float);
+  g.carry_bytes = (size_t)(g.axes * 2 * g.tiles * D) * sizeof(float);
   return DPG_OK;
 }
 
@@ -69,17 +72,25 @@ dpg_status check_states(const void* a, const void* b) {
   return aligned16(a) && aligned16(b) ? DPG_OK : DPG_ERR_ALIGNMENT;
 }
 
-const void* forward_fn(bool bf16, bool coupled) {
-  return bf16 ? (coupled ? (const void*)&recurrence_kernel<true, true> : (const void*)&recurrence_kernel<true, false>)
-              : (coupled ? (const void*)&recurrence_kernel<false, true> : (const void*)&recurrence_kernel<false, false>);
+const void* forward_fn(bool bf16, bool coupled, bool nt) {
+  static const void* const fns[2][2][2] = {
+      {{(const void*)&recurrence_kernel<false, false, false>, (const void*)&recurrence_kernel<false, false, true>},
+       {(const void*)&recurrence_kernel<false, true, false>, (const void*)&recurrence_kernel<false, true, true>}},
+      {{(const void*)&recurrence_kernel<true, false, false>, (const void*)&recurrence_kernel<true, false, true>},
+       {(const void*)&recurrence_kernel<true, true, false>, (const void*)&recurrence_kernel<true, true, true>}}};
+  return fns[bf16][coupled][nt];
 }
 const void* forward_span_fn(bool bf16, bool coupled) {
   return bf16 ? (coupled ? (const void*)&recurrence_span_kernel<true, true> : (const void*)&recurrence_span_kernel<true, false>)
               : (coupled ? (const void*)&recurrence_span_kernel<false, true> : (const void*)&recurrence_span_kernel<false, false>);
 }
-const void* dgrad_fn(bool bf16, bool coupled) {
-  return bf16 ? (coupled ? (const void*)&recurrence_dgrad_kernel<true, true> : (const void*)&recurrence_dgrad_kernel<true, false>)
-              : (coupled ? (const void*)&recurrence_dgrad_kernel<false, true> : (const void*)&recurrence_dgrad_kernel<false, false>);
+const void* dgrad_fn(bool bf16, bool coupled, bool nt) {
+  static const void* const fns[2][2][2] = {
+      {{(const void*)&recurrence_dgrad_kernel<false, false, false>, (const void*)&recurrence_dgrad_kernel<false, false, true>},
+       {(const void*)&recurrence_dgrad_kernel<false, true, false>, (const void*)&recurrence_dgrad_kernel<false, true, true>}},
+      {{(const void*)&recurrence_dgrad_kernel<true, false, false>, (const void*)&recurrence_dgrad_kernel<true, false, true>},
+       {(const void*)&recurrence_dgrad_kernel<true, true, false>, (const void*)&recurrence_dgrad_kernel<true, true, true>}}};
+  return fns[bf16][coupled][nt];
 }
 const void* dgrad_span_fn(bool bf16) {
   return bf16 ? (const void*)&recurrence_dgrad_span_kernel<true> : (const void*)&recurrence_dgrad_span_kernel<false>;
@@ -175,7 +186,7 @@ dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t 
     st = launch(forward_span_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
     if (st != DPG_OK) return st;
   }
-  return launch(forward_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
+  return launch(forward_fn(bf16, coupled != 0, past_caches(R, D, elt)), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
 }
 
 dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, int64_t ldg, const void* x, int64_t ldx,
@@ -221,7 +232,7 @@ dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, 
     st = launch(dgrad_span_fn(bf16), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
     if (st != DPG_OK) return st;
   }
-  return launch(dgrad_fn(bf16, coupled != 0), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
+  return launch(dgrad_fn(bf16, coupled != 0, past_caches(R, D, elt)), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
 }
 
 }  // extern "C"

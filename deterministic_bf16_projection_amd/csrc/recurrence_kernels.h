@@ -9,13 +9,12 @@
 //
 // Composition.  A run of rows maps the state before it to c -> A c + H, A the
 // product of its f and H its result from zero; two runs compose to (A1 A2, A2
-// H1 + H2).  A workgroup owns 64 channels and goes through its rows by tiles:
-// half a wave holds 64 channels of a run of eight rows, sixteen runs make a
-// tile.  The halves compose their runs, the waves meet in LDS, every lane finds
-// the state before its run, and then each row's, from values that stayed in
-// registers: the rows are read once.  A is zero only if some f is: products that
-// underflow are held at the smallest number, so that an infinite state stays
-// infinite.
+// H1 + H2).  A workgroup owns 128 channels, two to a lane, and goes through its
+// rows by tiles: each of its eight waves composes a run of U rows, the waves'
+// (A, H) meet in LDS, every wave finds the state before its run, and then each
+// row's, from values that stayed in registers: the rows are read once.  A is
+// zero only if some f is: products that underflow are held at the smallest
+// number, so that an infinite state stays infinite.
 //
 // Rows are grouped in axes, each a whole sequence or several short ones; a
 // sequence's first row takes f = 0 there and the initial state into its input.
@@ -25,9 +24,9 @@
 // instead of 3.  All of it depends on sizes alone, and every sum runs in a
 // fixed order.
 //
-// The forward pass can keep the FP32 state before each tile (1/64 of h's size
-// in BF16); the gradient recomputes the states in between from them instead of
-// reading rounded ones.
+// The forward pass can keep the FP32 state before every 64 rows (1/32 of h's
+// size in BF16); the gradient recomputes the states in between from them
+// instead of reading rounded ones.
 #pragma once
 #include <type_traits>
 
@@ -38,12 +37,14 @@ namespace dpg {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kRecChannels = 64;
-constexpr int kRecWaves = 8;
+constexpr int kRecChannels = 128;
+constexpr int kRecWaves = 8;              // runs of a tile
 constexpr int kRecThreads = 64 * kRecWaves;
-constexpr int kRecRuns = 2 * kRecWaves;  // of a tile
-constexpr int kRecRunRows = 8;
-constexpr int kRecTileRows = kRecRuns * kRecRunRows;
+constexpr int kRecRows = 16;              // of a run, forward and in the launch over spans
+constexpr int kRecGradRows = 8;           // of a run of the gradient
+constexpr int kRecTileRows = kRecWaves * kRecRows;
+constexpr int kRecCarryRows = kRecWaves * kRecGradRows;  // a tile of the gradient
+static_assert(kRecTileRows == 2 * kRecCarryRows, "two carries to a forward tile");
 
 struct RecParams {
   Rows8 gate, x, h, dh, dgate, dx;
@@ -51,13 +52,13 @@ struct RecParams {
   float* state_out;        // [S, D] after the last rows, or null
   const float* dstate;     // [S, D] gradient of the latter, or null: zeros
   float* dstate_out;       // [S, D] gradient of the former, or null
-  float* carries;          // [axes * tiles, D]
+  float* carries;          // [axes * 2 tiles, D]
   float* summary;          // [axes * spans, 2, D]: A, then H or Q
   const int32_t* seq;      // packed: each row's sequence, -1 behind the last
   int R, D, length;        // length: of every sequence, where they are not packed
   int axis_rows, tiles;    // of an axis
   int span_tiles, spans;
-  int blocks;              // of 64 channels
+  int blocks;              // of 128 channels
 };
 
 // ------------------------------------------------------------ two values --
@@ -83,8 +84,13 @@ __device__ __forceinline__ float weighted(float a, float b) { return mul_zero_wi
 __device__ __forceinline__ float carry_on(float a, float c, float b) { return weighted(a, c) + b; }
 // a product of weights: 0 exactly where the least of them is, else at least the
 // smallest normal number
-__device__ __forceinline__ float held(float product, float least) {
-  return fmaxf(product, fminf(least, 0x1p-126f));
+__device__ __forceinline__ float held(float product, float least) { return fmaxf(product, fminf(least, 0x1p-126f)); }
+// two runs, the first's values first
+__device__ __forceinline__ f32x2 rec_carry(const f32x2& A, const f32x2& c, const f32x2& H) {
+  return f32x2{carry_on(A[0], c[0], H[0]), carry_on(A[1], c[1], H[1])};
+}
+__device__ __forceinline__ f32x2 rec_product(const f32x2& A, const f32x2& B) {
+  return f32x2{held(A[0] * B[0], fminf(A[0], B[0])), held(A[1] * B[1], fminf(A[1], B[1]))};
 }
 
 // f and 1 - f, each to its own relative accuracy.  With e = exp(-gate), f = 1 /
@@ -114,22 +120,22 @@ __device__ __forceinline__ void gate_weights(float g, float& f, float& rest) {
 }
 
 // ---------------------------------------------------------------- places --
+// Everything but the channels is the same for a wave and lies in scalar
+// registers.
 struct RecPlace {
-  int lane, run, wave;    // of the run's 32 lanes; place in the tile
+  int lane, wave;
   int channel, safe;      // first of the lane's two channels, and one to load from
   bool live;              // the channels exist
   int begin, end;         // rows of the axis
   int first, last;        // tiles of the span
   int span;
-  int64_t tile0, span0;   // of the axis
+  int64_t carry0, span0;  // of the axis
 };
 __device__ __forceinline__ RecPlace rec_place(const RecParams& p) {
-  constexpr int TR = kRecTileRows;
   RecPlace q;
   const int id = blockIdx.x, rest = id / p.blocks, axis = rest / p.spans;
   q.span = rest - axis * p.spans;
-  q.lane = threadIdx.x & 31;
-  q.run = threadIdx.x >> 5;
+  q.lane = threadIdx.x & 63;
   q.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   q.channel = (id - rest * p.blocks) * kRecChannels + 2 * q.lane;
   q.live = q.channel < p.D;
@@ -137,108 +143,93 @@ __device__ __forceinline__ RecPlace rec_place(const RecParams& p) {
   q.begin = axis * p.axis_rows;
   q.end = min(p.R - q.begin, p.axis_rows) + q.begin;
   q.first = q.span * p.span_tiles;
-  q.last = min(q.first + p.span_tiles, (q.end - q.begin + TR - 1) / TR);
-  q.tile0 = (int64_t)axis * p.tiles;
+  q.last = min(q.first + p.span_tiles, (q.end - q.begin + kRecTileRows - 1) / kRecTileRows);
+  q.carry0 = (int64_t)axis * 2 * p.tiles;
   q.span0 = (int64_t)axis * p.spans;
   return q;
 }
 
-// One matrix as a lane sees it.  A block of rows (a tile, or a step of a span)
-// starts at a row that is the same for the workgroup and lies in a scalar
-// register; the lane's own offset from there stays the same from block to block.
-template <bool BF16>
+// One matrix as a lane sees it: the row's address lies in scalar registers, to
+// which an access adds the lane's offset by itself.  Without the empty
+// statement the compiler may add both up in vector registers.  NT: past the
+// caches.
+template <bool BF16, bool NT>
 struct RecRows {
-  const char* data;
+  char* data;
   int64_t pitch;     // bytes of a row
-  unsigned lane;     // bytes from the block's first row and column 0 to the lane's
-  unsigned column;   // bytes of the lane's column
-  __device__ __forceinline__ RecRows(const Rows8& m, int lane_row, int channel) {
-    constexpr int E = BF16 ? 2 : 4;
-    data = (const char*)m.data;
-    pitch = m.ld * E;
-    column = (unsigned)(channel * E);
-    lane = (unsigned)lane_row * (unsigned)pitch + column;
+  unsigned lane;     // byte of the lane's first channel
+  __device__ __forceinline__ RecRows(const Rows8& m, int channel)
+      : data((char*)m.data), pitch(m.ld * (BF16 ? 2 : 4)), lane((unsigned)channel * (BF16 ? 2u : 4u)) {}
+  __device__ __forceinline__ Raw2<BF16>* at(int64_t row) const {
+    char* base = data + row * pitch;
+    asm("" : "+s"(base));
+    return (Raw2<BF16>*)(base + lane);
   }
-  __device__ __forceinline__ Raw2<BF16> load(int64_t row, int u) const {
-    return *(const Raw2<BF16>*)(data + (row + u) * pitch + lane);
+  __device__ __forceinline__ Raw2<BF16> load(int64_t row) const {
+    return NT ? __builtin_nontemporal_load(at(row)) : *at(row);
   }
-  // row + r
-  __device__ __forceinline__ Raw2<BF16> load_row(int64_t row, int r) const {
-    return *(const Raw2<BF16>*)(data + row * pitch + ((unsigned)r * (unsigned)pitch + column));
-  }
-  __device__ __forceinline__ void store(int64_t row, int u, const Raw2<BF16>& v) const {
-    *(Raw2<BF16>*)(const_cast<char*>(data) + (row + u) * pitch + lane) = v;
+  __device__ __forceinline__ void store(int64_t row, const Raw2<BF16>& v) const {
+    if (NT)
+      __builtin_nontemporal_store(v, at(row));
+    else
+      *at(row) = v;
   }
 };
 
-// The same for the long runs of a span, which may lie more than 4 GB apart: a
-// pointer for each lane.
-template <bool BF16>
-struct RecRun {
-  const char* data;  // the run's first row
-  int64_t pitch;
-  __device__ __forceinline__ RecRun(const Rows8& m, int row, int channel) {
-    constexpr int E = BF16 ? 2 : 4;
-    pitch = m.ld * E;
-    data = (const char*)m.data + row * pitch + channel * E;
+// U rows of N matrices, loaded ahead of their use.  Rows behind the axis are
+// read from its last one.
+template <bool BF16, bool NT, int N, int U>
+struct RecFetch {
+  Raw2<BF16> raw[N][U];
+  int before, at;  // packed: lane l holds the sequences of rows l - 1 and l; rows outside the axis have -2
+  __device__ __forceinline__ void operator()(const RecParams& p, const RecPlace& q, const RecRows<BF16, NT>* const (&m)[N],
+                                             int row) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) raw[i][u] = m[i]->load(min(row + u, q.end - 1));
+    if (p.seq) {
+      const int r = row + q.lane;
+      before = q.lane <= U && r >= 1 && r <= q.end ? p.seq[r - 1] : -2;
+      at = q.lane <= U && r < q.end ? p.seq[r] : -2;
+    }
   }
-  __device__ __forceinline__ Raw2<BF16> load(int64_t r) const { return *(const Raw2<BF16>*)(data + r * pitch); }
 };
 
-// What is special about a run's rows: bit u for row u.  The lanes of a run
-// agree.
+// What is special about a run's rows: bit u for row u.
 struct RecEdges {
   unsigned live, start, last;
   int seq;     // sequence of the first row (not packed)
-};
-// packed: lane l of a run holds the sequences of rows l - 1 and l; rows outside
-// the axis have -2
-struct RecSeq {
-  int before, at;
+  bool plain;  // all rows live, none starts or ends a sequence
 };
 template <int U>
-__device__ __forceinline__ RecSeq rec_fetch_seq(const RecParams& p, const RecPlace& q, int row) {
-  const int r = row + q.lane;
-  RecSeq s;
-  s.before = q.lane <= U && r >= 1 && r <= q.end ? p.seq[r - 1] : -2;
-  s.at = q.lane <= U && r < q.end ? p.seq[r] : -2;
-  return s;
-}
-template <int U>
-__device__ __forceinline__ RecEdges rec_edges(const RecParams& p, const RecPlace& q, int row, const RecSeq& sq) {
-  RecEdges e{0, 0, 0, 0};
-  const unsigned full = (1u << U) - 1;
+__device__ __forceinline__ RecEdges rec_edges(const RecParams& p, const RecPlace& q, int row, int before, int at) {
+  RecEdges e{0, 0, 0, 0, false};
+  constexpr unsigned full = (1u << U) - 1;
   if (p.seq) {
-    const int shift = threadIdx.x & 32;
-    const unsigned differ = (unsigned)(__ballot(sq.at != sq.before) >> shift);
-    e.live = (unsigned)(__ballot(sq.at >= 0) >> shift) & full;
+    const unsigned differ = (unsigned)__ballot(at != before);
+    e.live = (unsigned)__ballot(at >= 0) & full;
     e.start = differ & e.live;
     e.last = (differ >> 1) & e.live;
+  } else if (p.length == p.axis_rows && row > q.begin && row + U < q.end) {
+    e.live = full;  // an axis is a sequence, and these rows are inside
   } else {
     const int n = min(max(q.end - row, 0), U);
     e.live = (1u << n) - 1;
     e.seq = row / p.length;
-    int at = row - e.seq * p.length;
+    int place = row - e.seq * p.length;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      e.start |= at == 0 ? 1u << u : 0;
-      ++at;
-      e.last |= at == p.length ? 1u << u : 0;
-      at = at == p.length ? 0 : at;
+      e.start |= place == 0 ? 1u << u : 0;
+      ++place;
+      e.last |= place == p.length ? 1u << u : 0;
+      place = place == p.length ? 0 : place;
     }
     e.start &= e.live;
     e.last &= e.live;
   }
+  e.plain = e.live == full && (e.start | e.last) == 0;
   return e;
-}
-// Whether rows [row, row + n) of an axis that is one sequence of equal ones
-// are all inside it and neither its first nor its last: known without a look at
-// each.
-__device__ __forceinline__ bool rec_inside(const RecParams& p, const RecPlace& q, int row, int n) {
-  return !p.seq && p.length == p.axis_rows && row > q.begin && row + n < q.end;
-}
-__device__ __forceinline__ bool rec_ordinary(const RecEdges& e, int U) {
-  return __ballot(e.live != (1u << U) - 1 || (e.start | e.last) != 0) == 0;
 }
 __device__ __forceinline__ int64_t rec_sequence(const RecParams& p, const RecEdges& e, int row, int u) {
   return p.seq ? p.seq[row + u] : e.seq + __builtin_popcount(e.start & ((2u << u) - 1) & ~1u);
@@ -253,47 +244,19 @@ __device__ __forceinline__ void rec_put_state(float* state, const RecParams& p, 
   if (state && q.live) *(f32x2*)(state + rec_sequence(p, e, row, u) * p.D + q.channel) = v;
 }
 
-// N matrices' rows of one run, loaded a block ahead of their use.
-template <bool BF16, int N, int U>
-struct RecFetch {
-  Raw2<BF16> raw[N][U];
-  RecSeq sq;
-  // the tile from `row` on, of which the lane has the rows from lane_row on
-  __device__ __forceinline__ void tile(const RecParams& p, const RecPlace& q, const RecRows<BF16>* const (&m)[N],
-                                       int row, int lane_row) {
-    if (row + kRecRuns * U <= q.end) {
+template <bool BF16, bool NT, int U>
+__device__ __forceinline__ void rec_store(const RecPlace& q, const RecRows<BF16, NT>& m, int row,
+                                          const Raw2<BF16> (&v)[U]) {
+  if (!q.live) return;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < N; ++i) raw[i][u] = m[i]->load(row, u);
-    } else {
-      // rows behind the axis are read from its last one
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = min(lane_row + u, q.end - 1 - row);
-#pragma unroll
-        for (int i = 0; i < N; ++i) raw[i][u] = m[i]->load_row(row, r);
-      }
-    }
-    if (p.seq) sq = rec_fetch_seq<U>(p, q, row + lane_row);
-  }
-  // rows [at, at + U) of the run that starts at run_row
-  __device__ __forceinline__ void run(const RecParams& p, const RecPlace& q, const RecRun<BF16>* const (&m)[N],
-                                      int run_row, int at, bool whole) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = whole ? at + u : min(at + u, q.end - 1 - min(run_row, q.end - 1));
-#pragma unroll
-      for (int i = 0; i < N; ++i) raw[i][u] = m[i]->load(r);
-    }
-    if (p.seq) sq = rec_fetch_seq<U>(p, q, run_row + at);
-  }
-};
+  for (int u = 0; u < U; ++u)
+    if (row + u < q.end) m.store(row + u, v[u]);
+}
 
 // --------------------------------------------------------------- forward --
 // f and b = w x of a run's rows.  Where the run is not plain, rows without a
 // sequence get zeros, and a first row f = 0 and the initial state in b.
-template <bool BF16, bool COUPLED, bool PLAIN, int U>
+template <bool BF16, bool COUPLED, int U>
 __device__ __forceinline__ void rec_inputs(const RecParams& p, const RecPlace& q, const RecEdges& e, int row,
                                            const Raw2<BF16> (&gate)[U], const Raw2<BF16> (&x)[U], f32x2 (&f)[U],
                                            f32x2 (&b)[U]) {
@@ -308,20 +271,15 @@ __device__ __forceinline__ void rec_inputs(const RecParams& p, const RecPlace& q
       b[u][k] = COUPLED ? weighted(rest, v[k]) : v[k];
     }
   }
-  if (PLAIN) return;
+  if (e.plain) return;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const bool live = e.live >> u & 1, start = e.start >> u & 1;
-    if (start) {
-      const f32x2 c = rec_state(p.state, p, e, q, row, u);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) b[u][k] = carry_on(f[u][k], c[k], b[u][k]);
+    const f32x2 zero = {0.f, 0.f};
+    if (e.start >> u & 1) {
+      b[u] = rec_carry(f[u], rec_state(p.state, p, e, q, row, u), b[u]);
+      f[u] = zero;
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      f[u][k] = live && !start ? f[u][k] : 0.f;
-      b[u][k] = live ? b[u][k] : 0.f;
-    }
+    if (!(e.live >> u & 1)) f[u] = b[u] = zero;
   }
 }
 
@@ -341,50 +299,10 @@ __device__ __forceinline__ void rec_compose(const f32x2 (&f)[U], const f32x2 (&b
   }
 }
 
-// Both halves' values of a wave, in all lanes: of run 2 w, and of run 2 w + 1.
-struct RecHalves {
-  f32x2 first, second;
-};
-__device__ __forceinline__ RecHalves rec_halves(const f32x2& v) {
-  RecHalves h;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    // (a bit cast of a vector's element itself would take the first one's)
-    const float value = v[k];
-    const unsigned bits = __builtin_bit_cast(unsigned, value);
-    const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
-    const unsigned lower = both[0], upper = both[1];
-    h.first[k] = __builtin_bit_cast(float, lower);
-    h.second[k] = __builtin_bit_cast(float, upper);
-  }
-  return h;
-}
-__device__ __forceinline__ f32x2 rec_carry(const f32x2& A, const f32x2& c, const f32x2& H) {
-  return f32x2{carry_on(A[0], c[0], H[0]), carry_on(A[1], c[1], H[1])};
-}
-__device__ __forceinline__ f32x2 rec_product(const f32x2& A, const f32x2& B) {
-  return f32x2{held(A[0] * B[0], fminf(A[0], B[0])), held(A[1] * B[1], fminf(A[1], B[1]))};
-}
-
-// The rows of a tile, one matrix's: all of them exist, or those before q.end.
-template <bool BF16, int U>
-__device__ __forceinline__ void rec_store(const RecPlace& q, const RecRows<BF16>& m, int row0, int row, bool whole,
-                                          const Raw2<BF16> (&v)[U]) {
-  if (!q.live) return;
-  if (whole) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) m.store(row0, u, v[u]);
-  } else {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (row + u < q.end) m.store(row0, u, v[u]);
-  }
-}
-
-template <bool BF16, bool COUPLED>
-__global__ void __launch_bounds__(kRecThreads) recurrence_kernel(RecParams p) {
-  constexpr int U = kRecRunRows, TR = kRecTileRows;
-  __shared__ f32x2 products[2][kRecWaves][32], results[2][kRecWaves][32];
+template <bool BF16, bool COUPLED, bool NT>
+__global__ void __launch_bounds__(kRecThreads, 2) recurrence_kernel(RecParams p) {
+  constexpr int U = kRecRows, TR = kRecTileRows;
+  __shared__ f32x2 products[2][kRecWaves][64], results[2][kRecWaves][64];
   const RecPlace q = rec_place(p);
   if (q.first >= q.last) return;
   f32x2 carry = {0.f, 0.f};
@@ -392,38 +310,33 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_kernel(RecParams p) {
     const float* at = p.summary + (q.span0 + s) * 2 * p.D + q.safe;
     carry = rec_carry(*(const f32x2*)at, carry, *(const f32x2*)(at + p.D));
   }
-  const int lane_row = q.run * U;
-  const bool second = q.run & 1;
-  const RecRows<BF16> gates(p.gate, lane_row, q.safe), xs(p.x, lane_row, q.safe), out(p.h, lane_row, q.channel);
-  const RecRows<BF16>* const in[2] = {&gates, &xs};
-  RecFetch<BF16, 2, U> next;
+  const RecRows<BF16, NT> gates(p.gate, q.safe), xs(p.x, q.safe), out(p.h, q.channel);
+  const RecRows<BF16, NT>* const in[2] = {&gates, &xs};
+  RecFetch<BF16, NT, 2, U> next;
   Raw2<BF16> done[U];
-  next.tile(p, q, in, q.begin + q.first * TR, lane_row);
-  for (int tile = q.first; tile < q.last; ++tile) {
-    const int row0 = q.begin + tile * TR, row = row0 + lane_row, turn = tile & 1;
-    const bool inside = rec_inside(p, q, row0, TR);
-    RecEdges e{};
-    if (!inside) e = rec_edges<U>(p, q, row, next.sq);
-    const bool plain = inside || rec_ordinary(e, U);
+  f32x2 start = carry;  // the state before the run of the tile before
+  int row = q.begin + q.first * TR + q.wave * U;
+  next(p, q, in, row);
+  for (int tile = q.first; tile < q.last; ++tile, row += TR) {
+    const int turn = tile & 1;
+    const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], b[U];
-    if (plain)
-      rec_inputs<BF16, COUPLED, true, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
-    else
-      rec_inputs<BF16, COUPLED, false, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
+    rec_inputs<BF16, COUPLED, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
     // Memory operations are waited for in the order of their issue: stores that
     // came after the next tile's loads would have to end before those are used.
     // So a tile's results are stored one tile later, before the loads.
-    if (tile > q.first) rec_store<BF16, U>(q, out, row0 - TR, row - TR, true, done);
-    if (p.carries && q.run == 0 && q.live) *(f32x2*)(p.carries + (q.tile0 + tile) * p.D + q.channel) = carry;
-    if (tile + 1 < q.last) next.tile(p, q, in, row0 + TR, lane_row);
+    const auto put = [&](int t, int r) {
+      rec_store<BF16, NT, U>(q, out, r, done);
+      if (p.carries && (q.wave & 3) == 0 && q.live)
+        *(f32x2*)(p.carries + (q.carry0 + 2 * t + (q.wave >> 2)) * p.D + q.channel) = start;
+    };
+    if (tile > q.first) put(tile - 1, row - TR);
+    if (tile + 1 < q.last) next(p, q, in, row + TR);
     f32x2 A = {1.f, 1.f}, H = {0.f, 0.f};
     rec_compose<U>(f, b, A, H);
-    const RecHalves As = rec_halves(A), Hs = rec_halves(H);
     // two places in LDS by turns: one barrier a tile
-    if (second)
-      products[turn][q.wave][q.lane] = rec_product(As.first, As.second);
-    else
-      results[turn][q.wave][q.lane] = rec_carry(As.second, Hs.first, Hs.second);
+    products[turn][q.wave][q.lane] = A;
+    results[turn][q.wave][q.lane] = H;
     __syncthreads();
     f32x2 h = carry;
 #pragma unroll
@@ -431,56 +344,46 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_kernel(RecParams p) {
       if (s == q.wave) h = carry;
       carry = rec_carry(products[turn][s][q.lane], carry, results[turn][s][q.lane]);
     }
-    const f32x2 over = rec_carry(As.first, h, Hs.first);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) h[k] = second ? over[k] : h[k];
+    start = h;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       h = rec_carry(f[u], h, b[u]);
       done[u] = pack2<BF16>(h);
-      if (!plain && (e.last >> u & 1)) rec_put_state(p.state_out, p, e, q, row, u, h);
+      if (e.last >> u & 1) rec_put_state(p.state_out, p, e, q, row, u, h);
     }
+    if (tile + 1 == q.last) put(tile, row);
   }
-  const int row0 = q.begin + (q.last - 1) * TR;
-  rec_store<BF16, U>(q, out, row0, row0 + lane_row, false, done);
 }
 
 // (A, H) of each span but an axis's last, whose rows' end nothing follows.  No
-// order is needed until the end, so that each run takes U span_tiles rows in
+// order is needed until the end, so that each wave takes U span_tiles rows in
 // one piece.
 template <bool BF16, bool COUPLED>
 __global__ void __launch_bounds__(kRecThreads) recurrence_span_kernel(RecParams p) {
-  constexpr int U = kRecRunRows, TR = kRecTileRows;
-  __shared__ f32x2 products[kRecRuns][32], results[kRecRuns][32];
+  constexpr int U = kRecRows;
+  __shared__ f32x2 products[kRecWaves][64], results[kRecWaves][64];
   const RecPlace q = rec_place(p);
   if (q.first >= q.last || q.span == p.spans - 1) return;
-  // every row of a span that is not its axis's last exists
-  const int run_row = q.begin + q.first * TR + q.run * p.span_tiles * U;
-  const RecRun<BF16> gates(p.gate, run_row, q.safe), xs(p.x, run_row, q.safe);
-  const RecRun<BF16>* const in[2] = {&gates, &xs};
-  const bool inside = rec_inside(p, q, q.begin + q.first * TR, p.span_tiles * TR);
+  const RecRows<BF16, false> gates(p.gate, q.safe), xs(p.x, q.safe);
+  const RecRows<BF16, false>* const in[2] = {&gates, &xs};
   f32x2 A = {1.f, 1.f}, H = {0.f, 0.f};
-  RecFetch<BF16, 2, U> next;
-  next.run(p, q, in, run_row, 0, true);
-  for (int at = 0; at < p.span_tiles * U; at += U) {
-    const int row = run_row + at;
-    RecEdges e{};
-    if (!inside) e = rec_edges<U>(p, q, row, next.sq);
+  RecFetch<BF16, false, 2, U> next;
+  int row = q.begin + q.first * kRecTileRows + q.wave * p.span_tiles * U;
+  const int end = row + p.span_tiles * U;
+  next(p, q, in, row);
+  for (; row < end; row += U) {
+    const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], b[U];
-    if (inside || rec_ordinary(e, U))
-      rec_inputs<BF16, COUPLED, true, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
-    else
-      rec_inputs<BF16, COUPLED, false, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
-    if (at + U < p.span_tiles * U) next.run(p, q, in, run_row, at + U, true);
+    rec_inputs<BF16, COUPLED, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
+    if (row + U < end) next(p, q, in, row + U);
     rec_compose<U>(f, b, A, H);
   }
-  products[q.run][q.lane] = A;
-  results[q.run][q.lane] = H;
+  products[q.wave][q.lane] = A;
+  results[q.wave][q.lane] = H;
   __syncthreads();
-  if (q.run != 0 || !q.live) return;
+  if (q.wave != 0 || !q.live) return;
 #pragma unroll
-  for (int s = 1; s < kRecRuns; ++s)
-  {
+  for (int s = 1; s < kRecWaves; ++s) {
     H = rec_carry(products[s][q.lane], H, results[s][q.lane]);
     A = rec_product(A, products[s][q.lane]);
   }
@@ -491,7 +394,7 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_span_kernel(RecParams 
 
 // -------------------------------------------------------------- gradient --
 // f and 1 - f of a run's rows, zeros at those without a sequence.
-template <bool BF16, bool PLAIN, int U>
+template <bool BF16, int U>
 __device__ __forceinline__ void rec_weights(const RecEdges& e, const Raw2<BF16> (&gate)[U], f32x2 (&f)[U],
                                             f32x2 (&rest)[U]) {
 #pragma unroll
@@ -501,44 +404,46 @@ __device__ __forceinline__ void rec_weights(const RecEdges& e, const Raw2<BF16> 
     for (int k = 0; k < 2; ++k) {
       float fk, rk;
       gate_weights<BF16>(g[k], fk, rk);
-      f[u][k] = PLAIN || (e.live >> u & 1) ? fk : 0.f;
-      rest[u][k] = PLAIN || (e.live >> u & 1) ? rk : 0.f;
+      f[u][k] = fk;
+      rest[u][k] = rk;
     }
   }
+  if (e.plain) return;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (!(e.live >> u & 1)) f[u] = rest[u] = f32x2{0.f, 0.f};
 }
 
 // dh of row u, with dstate at a last row
-template <bool BF16, bool PLAIN>
+template <bool BF16>
 __device__ __forceinline__ f32x2 rec_dh(const RecParams& p, const RecPlace& q, const RecEdges& e, int row, int u,
                                         const Raw2<BF16>& raw) {
   f32x2 d = unpack2(raw);
-  if (PLAIN) return d;
+  if (e.plain) return d;
   if (e.last >> u & 1) {
     const f32x2 more = rec_state(p.dstate, p, e, q, row, u);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) d[k] += more[k];
+    d = f32x2{d[0] + more[0], d[1] + more[1]};
   }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) d[k] = e.live >> u & 1 ? d[k] : 0.f;
+  if (!(e.live >> u & 1)) d = f32x2{0.f, 0.f};
   return d;
 }
 
 // A run backwards takes c, what reaches it from the rows after it, to A c + Q;
 // A is the same product as forward.
-template <bool BF16, bool PLAIN, int U>
+template <bool BF16, int U>
 __device__ __forceinline__ void rec_compose_back(const RecParams& p, const RecPlace& q, const RecEdges& e, int row,
                                                  const f32x2 (&f)[U], const Raw2<BF16> (&grad)[U], f32x2& A, f32x2& Q) {
   f32x2 least = A;
 #pragma unroll
   for (int u = U - 1; u >= 0; --u) {
-    const f32x2 dh = rec_dh<BF16, PLAIN>(p, q, e, row, u, grad[u]);
-    const bool stop = !PLAIN && (e.start >> u & 1);
+    const f32x2 dh = rec_dh<BF16>(p, q, e, row, u, grad[u]);
+    f32x2 fu = f[u];
+    if (e.start >> u & 1) fu = f32x2{0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float fk = stop ? 0.f : f[u][k];
-      A[k] *= fk;
-      least[k] = fminf(least[k], fk);
-      Q[k] = weighted(fk, dh[k] + Q[k]);
+      A[k] *= fu[k];
+      least[k] = fminf(least[k], fu[k]);
+      Q[k] = weighted(fu[k], dh[k] + Q[k]);
     }
   }
 #pragma unroll
@@ -548,14 +453,14 @@ __device__ __forceinline__ void rec_compose_back(const RecParams& p, const RecPl
 // The run's states from h, the one before it: before[u] is the state that row
 // u starts from.  Returns the last row's.  Rows without a sequence, which no
 // other follows, may give anything.
-template <bool BF16, bool COUPLED, bool PLAIN, int U>
+template <bool BF16, bool COUPLED, int U>
 __device__ __forceinline__ f32x2 rec_states(const RecParams& p, const RecPlace& q, const RecEdges& e, int row,
                                             const f32x2 (&f)[U], const f32x2 (&rest)[U], const Raw2<BF16> (&x)[U],
                                             f32x2 h, f32x2 (&before)[U]) {
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const f32x2 v = unpack2(x[u]);
-    if (!PLAIN && (e.start >> u & 1)) h = rec_state(p.state, p, e, q, row, u);
+    if (e.start >> u & 1) h = rec_state(p.state, p, e, q, row, u);
     before[u] = h;
 #pragma unroll
     for (int k = 0; k < 2; ++k) h[k] = carry_on(f[u][k], h[k], COUPLED ? weighted(rest[u][k], v[k]) : v[k]);
@@ -563,37 +468,10 @@ __device__ __forceinline__ f32x2 rec_states(const RecParams& p, const RecPlace& 
   return h;
 }
 
-template <bool BF16, bool COUPLED, bool PLAIN, int U>
-__device__ __forceinline__ void rec_finish(const RecParams& p, const RecPlace& q, const RecEdges& e, int row,
-                                           const f32x2 (&f)[U], const f32x2 (&rest)[U], const Raw2<BF16> (&x)[U],
-                                           const Raw2<BF16> (&grad)[U], const f32x2& h, f32x2 c, Raw2<BF16> (&dgate)[U],
-                                           Raw2<BF16> (&dx)[U]) {
-  f32x2 before[U];
-  rec_states<BF16, COUPLED, PLAIN, U>(p, q, e, row, f, rest, x, h, before);
-#pragma unroll
-  for (int u = U - 1; u >= 0; --u) {
-    const f32x2 v = unpack2(x[u]), dh = rec_dh<BF16, PLAIN>(p, q, e, row, u, grad[u]);
-    f32x2 out_x, out_g;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float g = dh[k] + c[k];
-      out_x[k] = COUPLED ? weighted(rest[u][k], g) : g;
-      out_g[k] = weighted(f[u][k] * rest[u][k], g * (COUPLED ? before[u][k] - v[k] : before[u][k]));
-      c[k] = weighted(f[u][k], g);
-    }
-    dx[u] = pack2<BF16>(out_x);
-    dgate[u] = pack2<BF16>(out_g);
-    if (!PLAIN && (e.start >> u & 1)) {
-      rec_put_state(p.dstate_out, p, e, q, row, u, c);
-      c = f32x2{0.f, 0.f};
-    }
-  }
-}
-
-template <bool BF16, bool COUPLED>
-__global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_kernel(RecParams p) {
-  constexpr int U = kRecRunRows, TR = kRecTileRows;
-  __shared__ f32x2 products[2][kRecWaves][32], results[2][kRecWaves][32], gradients[2][kRecWaves][32];
+template <bool BF16, bool COUPLED, bool NT>
+__global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecParams p) {
+  constexpr int U = kRecGradRows, TR = kRecCarryRows;
+  __shared__ f32x2 products[2][kRecWaves][64], results[2][kRecWaves][64], gradients[2][kRecWaves][64];
   const RecPlace q = rec_place(p);
   if (q.first >= q.last) return;
   f32x2 back = {0.f, 0.f};  // what reaches the tile from the rows after it
@@ -601,28 +479,22 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_kernel(RecParams
     const float* at = p.summary + (q.span0 + s) * 2 * p.D + q.safe;
     back = rec_carry(*(const f32x2*)at, back, *(const f32x2*)(at + p.D));
   }
-  const int lane_row = q.run * U;
-  const bool second = q.run & 1;
-  const RecRows<BF16> gates(p.gate, lane_row, q.safe), xs(p.x, lane_row, q.safe), dhs(p.dh, lane_row, q.safe);
-  const RecRows<BF16> dgate(p.dgate, lane_row, q.channel), dx(p.dx, lane_row, q.channel);
-  const RecRows<BF16>* const in[3] = {&gates, &xs, &dhs};
-  const auto carried = [&](int tile) { return *(const f32x2*)(p.carries + (q.tile0 + tile) * p.D + q.safe); };
-  RecFetch<BF16, 3, U> next;
+  const RecRows<BF16, NT> gates(p.gate, q.safe), xs(p.x, q.safe), dhs(p.dh, q.safe);
+  const RecRows<BF16, NT> dgate(p.dgate, q.channel), dx(p.dx, q.channel);
+  const RecRows<BF16, NT>* const in[3] = {&gates, &xs, &dhs};
+  const auto carried = [&](int tile) { return *(const f32x2*)(p.carries + (q.carry0 + tile) * p.D + q.safe); };
+  const int first = 2 * q.first, last = min(2 * q.last, (q.end - q.begin + TR - 1) / TR);  // tiles of 64 rows
+  RecFetch<BF16, NT, 3, U> next;
   Raw2<BF16> done_g[U], done_x[U];
-  next.tile(p, q, in, q.begin + (q.last - 1) * TR, lane_row);
-  f32x2 carry = carried(q.last - 1);
-  for (int tile = q.last - 1; tile >= q.first; --tile) {
-    const int row0 = q.begin + tile * TR, row = row0 + lane_row, turn = tile & 1;
-    const bool inside = rec_inside(p, q, row0, TR);
-    RecEdges e{};
-    if (!inside) e = rec_edges<U>(p, q, row, next.sq);
-    const bool plain = inside || rec_ordinary(e, U);
-    f32x2 f[U], rest[U], unused[U];
+  int row = q.begin + (last - 1) * TR + q.wave * U;
+  next(p, q, in, row);
+  f32x2 carry = carried(last - 1);
+  for (int tile = last - 1; tile >= first; --tile, row -= TR) {
+    const int turn = tile & 1;
+    const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
+    f32x2 f[U], rest[U], before[U];
     Raw2<BF16> v[U], dh[U];
-    if (plain)
-      rec_weights<BF16, true, U>(e, next.raw[0], f, rest);
-    else
-      rec_weights<BF16, false, U>(e, next.raw[0], f, rest);
+    rec_weights<BF16, U>(e, next.raw[0], f, rest);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u] = next.raw[1][u];
@@ -630,30 +502,21 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_kernel(RecParams
     }
     f32x2 h = carry;
     // one tile late, before the next loads, as in the forward pass
-    if (tile + 1 < q.last) {
-      const bool whole = row0 + 2 * TR <= q.end;
-      rec_store<BF16, U>(q, dgate, row0 + TR, row + TR, whole, done_g);
-      rec_store<BF16, U>(q, dx, row0 + TR, row + TR, whole, done_x);
-    }
-    if (tile > q.first) {
-      next.tile(p, q, in, row0 - TR, lane_row);
+    const auto put = [&](int r) {
+      rec_store<BF16, NT, U>(q, dgate, r, done_g);
+      rec_store<BF16, NT, U>(q, dx, r, done_x);
+    };
+    if (tile + 1 < last) put(row + TR);
+    if (tile > first) {
+      next(p, q, in, row - TR);
       carry = carried(tile - 1);
     }
     f32x2 A = {1.f, 1.f}, Q = {0.f, 0.f}, H = {0.f, 0.f};
-    if (plain) {
-      rec_compose_back<BF16, true, U>(p, q, e, row, f, dh, A, Q);
-      H = rec_states<BF16, COUPLED, true, U>(p, q, e, row, f, rest, v, H, unused);
-    } else {
-      rec_compose_back<BF16, false, U>(p, q, e, row, f, dh, A, Q);
-      H = rec_states<BF16, COUPLED, false, U>(p, q, e, row, f, rest, v, H, unused);
-    }
-    const RecHalves As = rec_halves(A), Hs = rec_halves(H), Qs = rec_halves(Q);
-    if (second) {
-      products[turn][q.wave][q.lane] = rec_product(As.first, As.second);
-    } else {
-      results[turn][q.wave][q.lane] = rec_carry(As.second, Hs.first, Hs.second);
-      gradients[turn][q.wave][q.lane] = rec_carry(As.first, Qs.second, Qs.first);
-    }
+    rec_compose_back<BF16, U>(p, q, e, row, f, dh, A, Q);
+    H = rec_states<BF16, COUPLED, U>(p, q, e, row, f, rest, v, H, before);
+    products[turn][q.wave][q.lane] = A;
+    results[turn][q.wave][q.lane] = H;
+    gradients[turn][q.wave][q.lane] = Q;
     __syncthreads();
     f32x2 c = back;
 #pragma unroll
@@ -664,63 +527,59 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_kernel(RecParams
       if (s == q.wave) c = back;
       back = rec_carry(products[turn][s][q.lane], back, gradients[turn][s][q.lane]);
     }
-    const f32x2 over = rec_carry(As.first, h, Hs.first), under = rec_carry(As.second, c, Qs.second);
+    rec_states<BF16, COUPLED, U>(p, q, e, row, f, rest, v, h, before);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      h[k] = second ? over[k] : h[k];
-      c[k] = second ? c[k] : under[k];
+    for (int u = U - 1; u >= 0; --u) {
+      const f32x2 xu = unpack2(v[u]), du = rec_dh<BF16>(p, q, e, row, u, dh[u]);
+      f32x2 out_x, out_g;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float g = du[k] + c[k];
+        out_x[k] = COUPLED ? weighted(rest[u][k], g) : g;
+        out_g[k] = weighted(f[u][k] * rest[u][k], g * (COUPLED ? before[u][k] - xu[k] : before[u][k]));
+        c[k] = weighted(f[u][k], g);
+      }
+      done_x[u] = pack2<BF16>(out_x);
+      done_g[u] = pack2<BF16>(out_g);
+      if (e.start >> u & 1) {
+        rec_put_state(p.dstate_out, p, e, q, row, u, c);
+        c = f32x2{0.f, 0.f};
+      }
     }
-    if (plain)
-      rec_finish<BF16, COUPLED, true, U>(p, q, e, row, f, rest, v, dh, h, c, done_g, done_x);
-    else
-      rec_finish<BF16, COUPLED, false, U>(p, q, e, row, f, rest, v, dh, h, c, done_g, done_x);
+    if (tile == first) put(row);
   }
-  const int row0 = q.begin + q.first * TR;
-  rec_store<BF16, U>(q, dgate, row0, row0 + lane_row, false, done_g);
-  rec_store<BF16, U>(q, dx, row0, row0 + lane_row, false, done_x);
 }
 
 // (A, Q) of each span but an axis's first.
 template <bool BF16>
 __global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_span_kernel(RecParams p) {
-  constexpr int U = kRecRunRows, TR = kRecTileRows;
-  __shared__ f32x2 products[kRecRuns][32], gradients[kRecRuns][32];
+  constexpr int U = kRecRows;
+  __shared__ f32x2 products[kRecWaves][64], gradients[kRecWaves][64];
   const RecPlace q = rec_place(p);
   if (q.first >= q.last || q.span == 0) return;
-  const int run_row = q.begin + q.first * TR + q.run * p.span_tiles * U, safe_row = min(run_row, q.end - 1);
-  const RecRun<BF16> gates(p.gate, safe_row, q.safe), dhs(p.dh, safe_row, q.safe);
-  const RecRun<BF16>* const in[2] = {&gates, &dhs};
-  const bool whole = q.begin + (q.first + p.span_tiles) * TR <= q.end;
-  const bool inside = rec_inside(p, q, q.begin + q.first * TR, p.span_tiles * TR);
+  const RecRows<BF16, false> gates(p.gate, q.safe), dhs(p.dh, q.safe);
+  const RecRows<BF16, false>* const in[2] = {&gates, &dhs};
   f32x2 A = {1.f, 1.f}, Q = {0.f, 0.f};
-  RecFetch<BF16, 2, U> next;
-  next.run(p, q, in, run_row, (p.span_tiles - 1) * U, whole);
-  for (int at = (p.span_tiles - 1) * U; at >= 0; at -= U) {
-    const int row = run_row + at;
-    RecEdges e{};
-    if (!inside) e = rec_edges<U>(p, q, row, next.sq);
-    const bool plain = inside || rec_ordinary(e, U);
+  RecFetch<BF16, false, 2, U> next;
+  const int begin = q.begin + q.first * kRecTileRows + q.wave * p.span_tiles * U;
+  int row = begin + (p.span_tiles - 1) * U;
+  next(p, q, in, row);
+  for (; row >= begin; row -= U) {
+    const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], rest[U];
     Raw2<BF16> dh[U];
-    if (plain)
-      rec_weights<BF16, true, U>(e, next.raw[0], f, rest);
-    else
-      rec_weights<BF16, false, U>(e, next.raw[0], f, rest);
+    rec_weights<BF16, U>(e, next.raw[0], f, rest);
 #pragma unroll
     for (int u = 0; u < U; ++u) dh[u] = next.raw[1][u];
-    if (at > 0) next.run(p, q, in, run_row, at - U, whole);
-    if (plain)
-      rec_compose_back<BF16, true, U>(p, q, e, row, f, dh, A, Q);
-    else
-      rec_compose_back<BF16, false, U>(p, q, e, row, f, dh, A, Q);
+    if (row > begin) next(p, q, in, row - U);
+    rec_compose_back<BF16, U>(p, q, e, row, f, dh, A, Q);
   }
-  products[q.run][q.lane] = A;
-  gradients[q.run][q.lane] = Q;
+  products[q.wave][q.lane] = A;
+  gradients[q.wave][q.lane] = Q;
   __syncthreads();
-  if (q.run != kRecRuns - 1 || !q.live) return;
+  if (q.wave != kRecWaves - 1 || !q.live) return;
 #pragma unroll
-  for (int s = kRecRuns - 2; s >= 0; --s)
-  {
+  for (int s = kRecWaves - 2; s >= 0; --s) {
     Q = rec_carry(products[s][q.lane], Q, gradients[s][q.lane]);
     A = rec_product(A, products[s][q.lane]);
   }
