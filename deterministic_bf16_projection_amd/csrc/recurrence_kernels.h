@@ -149,35 +149,73 @@ __device__ __forceinline__ RecPlace rec_place(const RecParams& p) {
   return q;
 }
 
-// One matrix as a lane sees it: the row's address lies in scalar registers, to
-// which an access adds the lane's offset by itself.  Without the empty
-// statement the compiler may add both up in vector registers.  NT: past the
-// caches.
+// One matrix as a lane sees it: a row's address lies in scalar registers, to
+// which an access adds the lane's offset by itself.  The empty statements keep
+// the compiler from adding both up in vector registers (of the offset it would
+// otherwise make 64 bits before the loop).  NT: past the caches.
 template <bool BF16, bool NT>
 struct RecRows {
-  char* data;
+  typedef __attribute__((address_space(1))) char* Bytes;
+  typedef __attribute__((address_space(1))) Raw2<BF16>* Values;
+  uint64_t data;
   int64_t pitch;     // bytes of a row
   unsigned lane;     // byte of the lane's first channel
   __device__ __forceinline__ RecRows(const Rows8& m, int channel)
-      : data((char*)m.data), pitch(m.ld * (BF16 ? 2 : 4)), lane((unsigned)channel * (BF16 ? 2u : 4u)) {}
-  __device__ __forceinline__ Raw2<BF16>* at(int64_t row) const {
-    char* base = data + row * pitch;
-    asm("" : "+s"(base));
-    return (Raw2<BF16>*)(base + lane);
+      : data((uint64_t)m.data), pitch(m.ld * (BF16 ? 2 : 4)), lane((unsigned)channel * (BF16 ? 2u : 4u)) {}
+
+  // U rows from `row` on; those behind the axis are its last one
+  template <int U>
+  __device__ __forceinline__ void load(const RecPlace& q, int row, Raw2<BF16> (&v)[U]) const {
+    unsigned offset = lane;
+    uint64_t base = data + min(row, q.end - 1) * pitch;
+    const auto get = [&](int u) {
+      asm volatile("" : "+s"(base), "+v"(offset));
+      const Values at = (Values)((Bytes)base + offset);
+      v[u] = NT ? __builtin_nontemporal_load(at) : *at;
+    };
+    if (row + U <= q.end) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        get(u);
+        base += pitch;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        get(u);
+        base += row + u + 1 < q.end ? pitch : 0;
+      }
+      asm volatile("" ::: "memory");  // not one set of loads for both branches
+    }
   }
-  __device__ __forceinline__ Raw2<BF16> load(int64_t row) const {
-    return NT ? __builtin_nontemporal_load(at(row)) : *at(row);
-  }
-  __device__ __forceinline__ void store(int64_t row, const Raw2<BF16>& v) const {
-    if (NT)
-      __builtin_nontemporal_store(v, at(row));
-    else
-      *at(row) = v;
+  // those of U rows that exist
+  template <int U>
+  __device__ __forceinline__ void store(const RecPlace& q, int row, const Raw2<BF16> (&v)[U]) const {
+    if (!q.live) return;
+    unsigned offset = lane;
+    uint64_t base = data + row * pitch;
+    const auto put = [&](int u) {
+      asm volatile("" : "+s"(base), "+v"(offset));
+      const Values at = (Values)((Bytes)base + offset);
+      if (NT)
+        __builtin_nontemporal_store(v[u], at);
+      else
+        *at = v[u];
+      base += pitch;
+    };
+    if (row + U <= q.end) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) put(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (row + u < q.end) put(u);
+      asm volatile("" ::: "memory");
+    }
   }
 };
 
-// U rows of N matrices, loaded ahead of their use.  Rows behind the axis are
-// read from its last one.
+// U rows of N matrices, loaded ahead of their use.
 template <bool BF16, bool NT, int N, int U>
 struct RecFetch {
   Raw2<BF16> raw[N][U];
@@ -185,9 +223,7 @@ struct RecFetch {
   __device__ __forceinline__ void operator()(const RecParams& p, const RecPlace& q, const RecRows<BF16, NT>* const (&m)[N],
                                              int row) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < N; ++i) raw[i][u] = m[i]->load(min(row + u, q.end - 1));
+    for (int i = 0; i < N; ++i) m[i]->load(q, row, raw[i]);
     if (p.seq) {
       const int r = row + q.lane;
       before = q.lane <= U && r >= 1 && r <= q.end ? p.seq[r - 1] : -2;
@@ -202,6 +238,15 @@ struct RecEdges {
   int seq;     // sequence of the first row (not packed)
   bool plain;  // all rows live, none starts or ends a sequence
 };
+// Work that depends on a run's edges, with a copy for plain runs, in which the
+// compiler leaves the questions out.
+template <int U, class F>
+__device__ __forceinline__ void rec_by_edges(const RecEdges& e, const F& work) {
+  if (e.plain)
+    work(RecEdges{(1u << U) - 1, 0, 0, 0, true});
+  else
+    work(e);
+}
 template <int U>
 __device__ __forceinline__ RecEdges rec_edges(const RecParams& p, const RecPlace& q, int row, int before, int at) {
   RecEdges e{0, 0, 0, 0, false};
@@ -244,15 +289,6 @@ __device__ __forceinline__ void rec_put_state(float* state, const RecParams& p, 
   if (state && q.live) *(f32x2*)(state + rec_sequence(p, e, row, u) * p.D + q.channel) = v;
 }
 
-template <bool BF16, bool NT, int U>
-__device__ __forceinline__ void rec_store(const RecPlace& q, const RecRows<BF16, NT>& m, int row,
-                                          const Raw2<BF16> (&v)[U]) {
-  if (!q.live) return;
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (row + u < q.end) m.store(row + u, v[u]);
-}
-
 // --------------------------------------------------------------- forward --
 // f and b = w x of a run's rows.  Where the run is not plain, rows without a
 // sequence get zeros, and a first row f = 0 and the initial state in b.
@@ -276,7 +312,7 @@ __device__ __forceinline__ void rec_inputs(const RecParams& p, const RecPlace& q
   for (int u = 0; u < U; ++u) {
     const f32x2 zero = {0.f, 0.f};
     if (e.start >> u & 1) {
-      b[u] = rec_carry(f[u], rec_state(p.state, p, e, q, row, u), b[u]);
+      if (p.state) b[u] = rec_carry(f[u], rec_state(p.state, p, e, q, row, u), b[u]);
       f[u] = zero;
     }
     if (!(e.live >> u & 1)) f[u] = b[u] = zero;
@@ -321,12 +357,14 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_kernel(RecParams p)
     const int turn = tile & 1;
     const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], b[U];
-    rec_inputs<BF16, COUPLED, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
+    rec_by_edges<U>(e, [&](const RecEdges& g) {
+      rec_inputs<BF16, COUPLED, U>(p, q, g, row, next.raw[0], next.raw[1], f, b);
+    });
     // Memory operations are waited for in the order of their issue: stores that
     // came after the next tile's loads would have to end before those are used.
     // So a tile's results are stored one tile later, before the loads.
     const auto put = [&](int t, int r) {
-      rec_store<BF16, NT, U>(q, out, r, done);
+      out.store(q, r, done);
       if (p.carries && (q.wave & 3) == 0 && q.live)
         *(f32x2*)(p.carries + (q.carry0 + 2 * t + (q.wave >> 2)) * p.D + q.channel) = start;
     };
@@ -345,12 +383,14 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_kernel(RecParams p)
       carry = rec_carry(products[turn][s][q.lane], carry, results[turn][s][q.lane]);
     }
     start = h;
+    rec_by_edges<U>(e, [&](const RecEdges& g) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      h = rec_carry(f[u], h, b[u]);
-      done[u] = pack2<BF16>(h);
-      if (e.last >> u & 1) rec_put_state(p.state_out, p, e, q, row, u, h);
-    }
+      for (int u = 0; u < U; ++u) {
+        h = rec_carry(f[u], h, b[u]);
+        done[u] = pack2<BF16>(h);
+        if (g.last >> u & 1) rec_put_state(p.state_out, p, g, q, row, u, h);
+      }
+    });
     if (tile + 1 == q.last) put(tile, row);
   }
 }
@@ -374,7 +414,9 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_span_kernel(RecParams 
   for (; row < end; row += U) {
     const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], b[U];
-    rec_inputs<BF16, COUPLED, U>(p, q, e, row, next.raw[0], next.raw[1], f, b);
+    rec_by_edges<U>(e, [&](const RecEdges& g) {
+      rec_inputs<BF16, COUPLED, U>(p, q, g, row, next.raw[0], next.raw[1], f, b);
+    });
     if (row + U < end) next(p, q, in, row + U);
     rec_compose<U>(f, b, A, H);
   }
@@ -494,7 +536,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecPar
     const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], rest[U], before[U];
     Raw2<BF16> v[U], dh[U];
-    rec_weights<BF16, U>(e, next.raw[0], f, rest);
+    rec_by_edges<U>(e, [&](const RecEdges& g) { rec_weights<BF16, U>(g, next.raw[0], f, rest); });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u] = next.raw[1][u];
@@ -503,8 +545,8 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecPar
     f32x2 h = carry;
     // one tile late, before the next loads, as in the forward pass
     const auto put = [&](int r) {
-      rec_store<BF16, NT, U>(q, dgate, r, done_g);
-      rec_store<BF16, NT, U>(q, dx, r, done_x);
+      dgate.store(q, r, done_g);
+      dx.store(q, r, done_x);
     };
     if (tile + 1 < last) put(row + TR);
     if (tile > first) {
@@ -512,8 +554,10 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecPar
       carry = carried(tile - 1);
     }
     f32x2 A = {1.f, 1.f}, Q = {0.f, 0.f}, H = {0.f, 0.f};
-    rec_compose_back<BF16, U>(p, q, e, row, f, dh, A, Q);
-    H = rec_states<BF16, COUPLED, U>(p, q, e, row, f, rest, v, H, before);
+    rec_by_edges<U>(e, [&](const RecEdges& g) {
+      rec_compose_back<BF16, U>(p, q, g, row, f, dh, A, Q);
+      H = rec_states<BF16, COUPLED, U>(p, q, g, row, f, rest, v, H, before);
+    });
     products[turn][q.wave][q.lane] = A;
     results[turn][q.wave][q.lane] = H;
     gradients[turn][q.wave][q.lane] = Q;
@@ -527,25 +571,27 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecPar
       if (s == q.wave) c = back;
       back = rec_carry(products[turn][s][q.lane], back, gradients[turn][s][q.lane]);
     }
-    rec_states<BF16, COUPLED, U>(p, q, e, row, f, rest, v, h, before);
+    rec_by_edges<U>(e, [&](const RecEdges& g) {
+      rec_states<BF16, COUPLED, U>(p, q, g, row, f, rest, v, h, before);
 #pragma unroll
-    for (int u = U - 1; u >= 0; --u) {
-      const f32x2 xu = unpack2(v[u]), du = rec_dh<BF16>(p, q, e, row, u, dh[u]);
-      f32x2 out_x, out_g;
+      for (int u = U - 1; u >= 0; --u) {
+        const f32x2 xu = unpack2(v[u]), du = rec_dh<BF16>(p, q, g, row, u, dh[u]);
+        f32x2 out_x, out_g;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float g = du[k] + c[k];
-        out_x[k] = COUPLED ? weighted(rest[u][k], g) : g;
-        out_g[k] = weighted(f[u][k] * rest[u][k], g * (COUPLED ? before[u][k] - xu[k] : before[u][k]));
-        c[k] = weighted(f[u][k], g);
+        for (int k = 0; k < 2; ++k) {
+          const float r = du[k] + c[k];
+          out_x[k] = COUPLED ? weighted(rest[u][k], r) : r;
+          out_g[k] = weighted(f[u][k] * rest[u][k], r * (COUPLED ? before[u][k] - xu[k] : before[u][k]));
+          c[k] = weighted(f[u][k], r);
+        }
+        done_x[u] = pack2<BF16>(out_x);
+        done_g[u] = pack2<BF16>(out_g);
+        if (g.start >> u & 1) {
+          rec_put_state(p.dstate_out, p, g, q, row, u, c);
+          c = f32x2{0.f, 0.f};
+        }
       }
-      done_x[u] = pack2<BF16>(out_x);
-      done_g[u] = pack2<BF16>(out_g);
-      if (e.start >> u & 1) {
-        rec_put_state(p.dstate_out, p, e, q, row, u, c);
-        c = f32x2{0.f, 0.f};
-      }
-    }
+    });
     if (tile == first) put(row);
   }
 }
@@ -568,11 +614,11 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_dgrad_span_kernel(RecP
     const RecEdges e = rec_edges<U>(p, q, row, next.before, next.at);
     f32x2 f[U], rest[U];
     Raw2<BF16> dh[U];
-    rec_weights<BF16, U>(e, next.raw[0], f, rest);
+    rec_by_edges<U>(e, [&](const RecEdges& g) { rec_weights<BF16, U>(g, next.raw[0], f, rest); });
 #pragma unroll
     for (int u = 0; u < U; ++u) dh[u] = next.raw[1][u];
     if (row > begin) next(p, q, in, row - U);
-    rec_compose_back<BF16, U>(p, q, e, row, f, dh, A, Q);
+    rec_by_edges<U>(e, [&](const RecEdges& g) { rec_compose_back<BF16, U>(p, q, g, row, f, dh, A, Q); });
   }
   products[q.wave][q.lane] = A;
   gradients[q.wave][q.lane] = Q;
