@@ -84,6 +84,10 @@ const void* forward_span_fn(bool bf16, bool coupled) {
   return bf16 ? (coupled ? (const void*)&recurrence_span_kernel<true, true> : (const void*)&recurrence_span_kernel<true, false>)
               : (coupled ? (const void*)&recurrence_span_kernel<false, true> : (const void*)&recurrence_span_kernel<false, false>);
 }
+const void* step_fn(bool bf16, bool coupled) {
+  return bf16 ? (coupled ? (const void*)&recurrence_step_kernel<true, true> : (const void*)&recurrence_step_kernel<true, false>)
+              : (coupled ? (const void*)&recurrence_step_kernel<false, true> : (const void*)&recurrence_step_kernel<false, false>);
+}
 const void* dgrad_fn(bool bf16, bool coupled, bool nt) {
   static const void* const fns[2][2][2] = {
       {{(const void*)&recurrence_dgrad_kernel<false, false, false>, (const void*)&recurrence_dgrad_kernel<false, false, true>},
@@ -172,6 +176,11 @@ dpg_status dpg_recurrence(const void* gate, int64_t ldg, const void* x, int64_t 
                                D, stream)) != DPG_OK)
     return st;
   void* args[] = {&p};
+  // Sequences of one row: 32 of them, 4096 channels, 7.9 us by tiles, 6.3
+  // row by row (both mostly the call).  The gradient finds the states itself where every row is a first
+  // one, so that the carries need no values.
+  if (!packed && S == R)
+    return launch(step_fn(bf16, coupled != 0), std::min<int64_t>((R * (D / 8) + 255) / 256, 1 << 16), 256, 0, args, stream);
   if (g.spans > 1) {
     if (state && state == state_out) {
       // a sequence's last span may write its state before the first has read it
@@ -232,7 +241,8 @@ dpg_status dpg_recurrence_dgrad(const void* dh, int64_t lddh, const void* gate, 
     st = launch(dgrad_span_fn(bf16), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
     if (st != DPG_OK) return st;
   }
-  return launch(dgrad_fn(bf16, coupled != 0, past_caches(R, D, elt)), g.axes * g.spans * g.blocks, kRecThreads, 0, args, stream);
+  return launch(dgrad_fn(bf16, coupled != 0, past_caches(R, D, elt)), g.axes * g.spans * g.blocks, kRecGradThreads,
+                0, args, stream);
 }
 
 }  // extern "C"

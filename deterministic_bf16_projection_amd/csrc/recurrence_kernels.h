@@ -10,7 +10,7 @@
 // Composition.  A run of rows maps the state before it to c -> A c + H, A the
 // product of its f and H its result from zero; two runs compose to (A1 A2, A2
 // H1 + H2).  A workgroup owns 128 channels, two to a lane, and goes through its
-// rows by tiles: each of its eight waves composes a run of U rows, the waves'
+// rows by tiles: each of its waves composes a run of eight rows, the waves'
 // (A, H) meet in LDS, every wave finds the state before its run, and then each
 // row's, from values that stayed in registers: the rows are read once.  A is
 // zero only if some f is: products that underflow are held at the smallest
@@ -38,12 +38,13 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kRecChannels = 128;
-constexpr int kRecWaves = 8;              // runs of a tile
-constexpr int kRecThreads = 64 * kRecWaves;
-constexpr int kRecRows = 16;              // of a run, forward and in the launch over spans
-constexpr int kRecGradRows = 8;           // of a run of the gradient
+// Runs of a tile (waves), and rows of a run: forward and in the launches over
+// spans, and of the gradient, whose registers allow two waves to a SIMD.
+constexpr int kRecWaves = 16, kRecRows = 8;
+constexpr int kRecGradWaves = 8, kRecGradRows = 8;
+constexpr int kRecThreads = 64 * kRecWaves, kRecGradThreads = 64 * kRecGradWaves;
 constexpr int kRecTileRows = kRecWaves * kRecRows;
-constexpr int kRecCarryRows = kRecWaves * kRecGradRows;  // a tile of the gradient
+constexpr int kRecCarryRows = kRecGradWaves * kRecGradRows;
 static_assert(kRecTileRows == 2 * kRecCarryRows, "two carries to a forward tile");
 
 struct RecParams {
@@ -336,7 +337,7 @@ __device__ __forceinline__ void rec_compose(const f32x2 (&f)[U], const f32x2 (&b
 }
 
 template <bool BF16, bool COUPLED, bool NT>
-__global__ void __launch_bounds__(kRecThreads, 2) recurrence_kernel(RecParams p) {
+__global__ void __launch_bounds__(kRecThreads) recurrence_kernel(RecParams p) {
   constexpr int U = kRecRows, TR = kRecTileRows;
   __shared__ f32x2 products[2][kRecWaves][64], results[2][kRecWaves][64];
   const RecPlace q = rec_place(p);
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_kernel(RecParams p)
     // So a tile's results are stored one tile later, before the loads.
     const auto put = [&](int t, int r) {
       out.store(q, r, done);
-      if (p.carries && (q.wave & 3) == 0 && q.live)
-        *(f32x2*)(p.carries + (q.carry0 + 2 * t + (q.wave >> 2)) * p.D + q.channel) = start;
+      if (p.carries && q.wave % (kRecWaves / 2) == 0 && q.live)
+        *(f32x2*)(p.carries + (q.carry0 + 2 * t + q.wave / (kRecWaves / 2)) * p.D + q.channel) = start;
     };
     if (tile > q.first) put(tile - 1, row - TR);
     if (tile + 1 < q.last) next(p, q, in, row + TR);
@@ -432,6 +433,38 @@ __global__ void __launch_bounds__(kRecThreads) recurrence_span_kernel(RecParams 
   float* at = p.summary + (q.span0 + q.span) * 2 * p.D + q.channel;
   *(f32x2*)at = A;
   *(f32x2*)(at + p.D) = H;
+}
+
+// Sequences of one row each, a generation step: nothing to compose, eight
+// channels to a thread and one row after the other.
+template <bool BF16, bool COUPLED>
+__global__ void __launch_bounds__(256) recurrence_step_kernel(RecParams p) {
+  const int groups = p.D >> 3;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.R * groups; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / groups;
+    const int group = (int)(i - row * groups);
+    float g[8], x[8], h[8];
+    const Raw8<BF16> gates = load8<BF16>(p.gate, row, group), xs = load8<BF16>(p.x, row, group);
+    f32x4 c[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const int64_t at = row * p.D + 8 * group;
+    if (p.state) {
+      c[0] = *(const f32x4*)(p.state + at);
+      c[1] = *(const f32x4*)(p.state + at + 4);
+    }
+    unpack8(gates, g);
+    unpack8(xs, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float f, rest;
+      gate_weights<BF16>(g[j], f, rest);
+      h[j] = carry_on(f, c[j >> 2][j & 3], COUPLED ? weighted(rest, x[j]) : x[j]);
+    }
+    store8<BF16>(p.h, row, group, h);
+    if (p.state_out) {
+      *(f32x4*)(p.state_out + at) = f32x4{h[0], h[1], h[2], h[3]};
+      *(f32x4*)(p.state_out + at + 4) = f32x4{h[4], h[5], h[6], h[7]};
+    }
+  }
 }
 
 // -------------------------------------------------------------- gradient --
@@ -511,9 +544,9 @@ __device__ __forceinline__ f32x2 rec_states(const RecParams& p, const RecPlace& 
 }
 
 template <bool BF16, bool COUPLED, bool NT>
-__global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecParams p) {
+__global__ void __launch_bounds__(kRecGradThreads, 2) recurrence_dgrad_kernel(RecParams p) {
   constexpr int U = kRecGradRows, TR = kRecCarryRows;
-  __shared__ f32x2 products[2][kRecWaves][64], results[2][kRecWaves][64], gradients[2][kRecWaves][64];
+  __shared__ f32x2 products[2][kRecGradWaves][64], results[2][kRecGradWaves][64], gradients[2][kRecGradWaves][64];
   const RecPlace q = rec_place(p);
   if (q.first >= q.last) return;
   f32x2 back = {0.f, 0.f};  // what reaches the tile from the rows after it
@@ -564,10 +597,10 @@ __global__ void __launch_bounds__(kRecThreads, 2) recurrence_dgrad_kernel(RecPar
     __syncthreads();
     f32x2 c = back;
 #pragma unroll
-    for (int s = 0; s < kRecWaves - 1; ++s)
+    for (int s = 0; s < kRecGradWaves - 1; ++s)
       if (s < q.wave) h = rec_carry(products[turn][s][q.lane], h, results[turn][s][q.lane]);
 #pragma unroll
-    for (int s = kRecWaves - 1; s >= 0; --s) {
+    for (int s = kRecGradWaves - 1; s >= 0; --s) {
       if (s == q.wave) c = back;
       back = rec_carry(products[turn][s][q.lane], back, gradients[turn][s][q.lane]);
     }
