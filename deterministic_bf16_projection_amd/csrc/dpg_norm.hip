@@ -18,46 +18,76 @@ Rows8 rows8(const void* data, int64_t ld) { return Rows8{const_cast<void*>(data)
 
 constexpr int64_t kMaxRows = (1ll << 31) - 1;
 
-// Waves of a row and groups of eight columns of a lane.
+constexpr int64_t kNormColumns = kNormWaves * 1024;
 struct NormLayout {
-  int waves, groups;
-  int columns() const { return waves * groups * 512; }
+  int chunks, waves, sets;  // groups of eight columns of a lane; waves of a row; rows of a workgroup at once
 };
-constexpr NormLayout kNormLayouts[] = {{1, 1}, {1, 2}, {4, 1}, {4, 2}, {4, 3}, {4, 4}, {8, 3}, {8, 4}};
-constexpr int64_t kNormColumns = 8 * 4 * 512;
-
-int norm_layout(int64_t H) {
-  int i = 0;
-  while (kNormLayouts[i].columns() < H) ++i;
-  return i;
+// Forward.  Few rows, and sums: up to two groups to a lane, weights in
+// registers, so that a row's latency is spread over waves.  Many rows: as few
+// waves to a row as hold it with eight groups to a lane, so that none waits for
+// others (16384 rows of 4096 columns, BF16: one wave 47.8 us, four 52, eight 62;
+// sums of 8192 rows, FP32 and BF16: two waves 81 us, four 78).
+constexpr int64_t kNormManyRows = 1024;
+NormLayout norm_layout(int64_t T, int64_t H, bool add) {
+  NormLayout l;
+  if (T < kNormManyRows || H <= 1024 || add)
+    l.chunks = H <= 512 ? 1 : 2;
+  else
+    l.chunks = H <= 2048 ? 4 : 8;
+  l.waves = (int)((H + 512 * l.chunks - 1) / (512 * l.chunks));
+  // workgroups of enough waves for eight to a CU with their weights in LDS
+  l.sets = std::max(1, (norm_shares_weights(l.chunks) && H > 4096 ? 8 : 4) / l.waves);
+  return l;
 }
-
-// Workgroups of the gradient: each one's sums for the weight gradient are a row
-// of the workspace, so there are no more than fill the CUs, and each has at
-// least eight rounds of rows where there are so many.
-constexpr int64_t kGradBlocks = 512;
+// workgroups that go through all rows: 2 to 8 to a CU
+int64_t norm_grid(const NormLayout& l) { return norm_shares_weights(l.chunks) ? 512 : 2048; }
+// Gradient: one group to a lane as long as sixteen waves hold the row (two need
+// more registers than sixteen waves have), and as many rows at once as sixteen
+// waves hold, since each workgroup's sums for the weight gradient are a row of
+// the workspace.
+NormLayout grad_layout(int64_t H) {
+  NormLayout l;
+  l.chunks = H <= kNormWaves * 512 ? 1 : 2;
+  l.waves = (int)((H + 512 * l.chunks - 1) / (512 * l.chunks));
+  l.sets = kNormWaves / l.waves;
+  return l;
+}
+// One workgroup to a CU, and at least two rows of each set where there are so many.
+constexpr int64_t kGradBlocks = 256;
 int64_t grad_blocks(int64_t T, int64_t H) {
-  const int64_t rounds = (T + norm_rows(kNormLayouts[norm_layout(H)].waves) - 1) / norm_rows(kNormLayouts[norm_layout(H)].waves);
-  return std::min(kGradBlocks, (rounds + 7) / 8);
+  const int64_t each = 2 * grad_layout(H).sets;
+  return std::min(kGradBlocks, (T + each - 1) / each);
 }
 
-template <bool X_BF16, bool ADD>
-const void* norm_fn(int layout) {
-  static const void* const fns[] = {
-      (const void*)&norm_kernel<X_BF16, 1, 1, ADD>, (const void*)&norm_kernel<X_BF16, 1, 2, ADD>,
-      (const void*)&norm_kernel<X_BF16, 4, 1, ADD>, (const void*)&norm_kernel<X_BF16, 4, 2, ADD>,
-      (const void*)&norm_kernel<X_BF16, 4, 3, ADD>, (const void*)&norm_kernel<X_BF16, 4, 4, ADD>,
-      (const void*)&norm_kernel<X_BF16, 8, 3, ADD>, (const void*)&norm_kernel<X_BF16, 8, 4, ADD>};
-  return fns[layout];
+template <bool X, bool Y, int C>
+const void* norm_fn(bool add, bool branch) {
+  if constexpr (norm_shares_weights(C)) return (const void*)&norm_kernel<X, Y, C, false, X>;
+  return !add ? (const void*)&norm_kernel<X, Y, C, false, X>
+              : branch ? (const void*)&norm_kernel<X, Y, C, true, true> : (const void*)&norm_kernel<X, Y, C, true, false>;
 }
-template <bool X_BF16, bool ADD>
-const void* norm_dgrad_fn(int layout) {
-  static const void* const fns[] = {
-      (const void*)&norm_dgrad_kernel<X_BF16, 1, 1, ADD>, (const void*)&norm_dgrad_kernel<X_BF16, 1, 2, ADD>,
-      (const void*)&norm_dgrad_kernel<X_BF16, 4, 1, ADD>, (const void*)&norm_dgrad_kernel<X_BF16, 4, 2, ADD>,
-      (const void*)&norm_dgrad_kernel<X_BF16, 4, 3, ADD>, (const void*)&norm_dgrad_kernel<X_BF16, 4, 4, ADD>,
-      (const void*)&norm_dgrad_kernel<X_BF16, 8, 3, ADD>, (const void*)&norm_dgrad_kernel<X_BF16, 8, 4, ADD>};
-  return fns[layout];
+template <int C>
+const void* norm_fn(bool x, bool y, bool add, bool branch) {
+  return x ? (y ? norm_fn<true, true, C>(add, branch) : norm_fn<true, false, C>(add, branch))
+           : (y ? norm_fn<false, true, C>(add, branch) : norm_fn<false, false, C>(add, branch));
+}
+const void* norm_fn(int chunks, bool x, bool y, bool add, bool branch) {
+  switch (chunks) {
+    case 1: return norm_fn<1>(x, y, add, branch);
+    case 2: return norm_fn<2>(x, y, add, branch);
+    case 4: return norm_fn<4>(x, y, add, branch);
+    default: return norm_fn<8>(x, y, add, branch);
+  }
+}
+template <bool X, bool Y>
+const void* dropout_fn(bool add, bool past) {
+  if (add) return past ? (const void*)&dropout_kernel<X, Y, true, true> : (const void*)&dropout_kernel<X, Y, true, false>;
+  return past ? (const void*)&dropout_kernel<X, Y, false, true> : (const void*)&dropout_kernel<X, Y, false, false>;
+}
+template <bool X, bool DY>
+const void* norm_dgrad_fn(int chunks, bool add) {
+  if (add)
+    return chunks == 1 ? (const void*)&norm_dgrad_kernel<X, DY, 1, true> : (const void*)&norm_dgrad_kernel<X, DY, 2, true>;
+  return chunks == 1 ? (const void*)&norm_dgrad_kernel<X, DY, 1, false> : (const void*)&norm_dgrad_kernel<X, DY, 2, false>;
 }
 
 dpg_status check_norm(int64_t T, int64_t H) {
@@ -91,40 +121,42 @@ dpg_status drop_params(const dpg_dropout_options* o, DropParams& d) {
   return DPG_OK;
 }
 
-dpg_status run_norm(NormParams& p, bool x_bf16, bool add, int64_t T, int64_t H, double eps, hipStream_t stream) {
+dpg_status run_norm(NormParams& p, bool x_bf16, bool y_bf16, bool add, bool branch_bf16, int64_t T, int64_t H,
+                    double eps, hipStream_t stream) {
+  const NormLayout l = norm_layout(T, H, add);
   p.T = T;
   p.H = (int)H;
+  p.waves = l.waves;
+  p.groups = l.sets;
   p.inv_h = 1.f / (float)H;
   p.eps = (float)eps;
-  const int layout = norm_layout(H);
-  const int waves = kNormLayouts[layout].waves;
-  const void* fn = x_bf16 ? (add ? norm_fn<true, true>(layout) : norm_fn<true, false>(layout))
-                          : (add ? norm_fn<false, true>(layout) : norm_fn<false, false>(layout));
+  const void* fn = norm_fn(l.chunks, x_bf16, y_bf16, add, branch_bf16);
+  const size_t lds = norm_shares_weights(l.chunks) ? (size_t)H * 2 * sizeof(float) : 0;
   void* args[] = {&p};
-  return launch(fn, std::min<int64_t>((T + norm_rows(waves) - 1) / norm_rows(waves), 2048), norm_threads(waves), 0,
-                args, stream);
+  return launch(fn, std::min<int64_t>((T + l.sets - 1) / l.sets, norm_grid(l)), 64 * l.waves * l.sets, lds, args, stream);
 }
 
-dpg_status run_norm_grad(NormGradParams& p, bool x_bf16, bool add, int64_t T, int64_t H, float* dweight, float* dbias,
-                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+dpg_status run_norm_grad(NormGradParams& p, bool x_bf16, bool dy_bf16, bool add, int64_t T, int64_t H, float* dweight,
+                         float* dbias, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const bool sums = dweight || dbias;
   if (sums && T > 0) {
     const size_t need = dpg_layer_norm_workspace_size(T, H);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DPG_ERR_WORKSPACE;
     p.partial = (float*)workspace;
   }
+  const NormLayout l = grad_layout(H);
   p.T = T;
   p.H = (int)H;
-  p.inv_h = 1.f / (float)H;
+  p.waves = l.waves;
+  p.groups = l.sets;
   int blocks = 0;
   if (T > 0) {
     blocks = (int)grad_blocks(T, H);
-    const int layout = norm_layout(H);
-    const int waves = kNormLayouts[layout].waves;
-    const void* fn = x_bf16 ? (add ? norm_dgrad_fn<true, true>(layout) : norm_dgrad_fn<true, false>(layout))
-                            : (add ? norm_dgrad_fn<false, true>(layout) : norm_dgrad_fn<false, false>(layout));
+    const void* fn = x_bf16 ? (dy_bf16 ? norm_dgrad_fn<true, true>(l.chunks, add) : norm_dgrad_fn<true, false>(l.chunks, add))
+                            : (dy_bf16 ? norm_dgrad_fn<false, true>(l.chunks, add) : norm_dgrad_fn<false, false>(l.chunks, add));
+    const size_t lds = sums && l.sets > 1 ? (size_t)l.sets * H * sizeof(float) : 0;
     void* args[] = {&p};
-    const dpg_status st = launch(fn, blocks, norm_threads(waves), 0, args, stream);
+    const dpg_status st = launch(fn, blocks, 64 * l.waves * l.sets, lds, args, stream);
     if (st != DPG_OK) return st;
   }
   if (!sums) return DPG_OK;
@@ -154,12 +186,14 @@ dpg_status dpg_dropout(const void* x, int64_t ldx, dpg_dtype x_dtype, const void
   if ((st = check_mat(Mat{y, ldy, T, H, elt_size((int)y_dtype)})) != DPG_OK) return st;
   if (residual && (st = check_mat(Mat{residual, ldr, T, H, elt_size((int)y_dtype)})) != DPG_OK) return st;
   if (T == 0 || H == 0) return DPG_OK;
+  // outputs that do not fit the XCDs' 32 MB of L2 go past it, and so do their inputs
+  const bool past = T * H >= (int64_t)(32 << 20) / elt_size((int)y_dtype);
   p.T = T;
   p.per_row = (int)(H / 8);
   p.groups = T * (H / 8);
   // rows that follow each other without gaps are one long row, cut where it suits the workgroups
   if (T > 1 ? ldx == H && ldy == H && (!residual || ldr == H) : true) {
-    constexpr int kGroups = 2048;
+    constexpr int kGroups = 512;
     p.per_row = kGroups;
     p.T = (p.groups + kGroups - 1) / kGroups;
     ldx = ldy = ldr = 8 * kGroups;
@@ -169,12 +203,10 @@ dpg_status dpg_dropout(const void* x, int64_t ldx, dpg_dtype x_dtype, const void
   p.residual = rows8(residual, ldr);
   p.lanes_log2 = 3;
   while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < std::min<int64_t>(p.per_row, p.groups)) ++p.lanes_log2;
-  const bool a = x_dtype == DPG_BF16, b = y_dtype == DPG_BF16;
-  const void* fn =
-      residual ? (a ? (b ? (const void*)&dropout_kernel<true, true, true> : (const void*)&dropout_kernel<true, false, true>)
-                    : (b ? (const void*)&dropout_kernel<false, true, true> : (const void*)&dropout_kernel<false, false, true>))
-               : (a ? (b ? (const void*)&dropout_kernel<true, true, false> : (const void*)&dropout_kernel<true, false, false>)
-                    : (b ? (const void*)&dropout_kernel<false, true, false> : (const void*)&dropout_kernel<false, false, false>));
+  const bool add = residual != nullptr;
+  const void* fn = x_dtype == DPG_BF16
+                       ? (y_dtype == DPG_BF16 ? dropout_fn<true, true>(add, past) : dropout_fn<true, false>(add, past))
+                       : (y_dtype == DPG_BF16 ? dropout_fn<false, true>(add, past) : dropout_fn<false, false>(add, past));
   const int64_t each = 256 >> p.lanes_log2;
   void* args[] = {&p};
   return launch(fn, std::min<int64_t>((p.T + each - 1) / each, 1 << 22), 256, 0, args, stream);
@@ -198,8 +230,7 @@ dpg_status dpg_layer_norm(const void* x, int64_t ldx, dpg_dtype x_dtype, const f
   p.bias = bias;
   p.mean = mean;
   p.rstd = rstd;
-  p.y_bf16 = y_dtype == DPG_BF16;
-  return run_norm(p, x_dtype == DPG_BF16, false, T, H, eps, stream);
+  return run_norm(p, x_dtype == DPG_BF16, y_dtype == DPG_BF16, false, false, T, H, eps, stream);
 }
 
 dpg_status dpg_add_layer_norm(const void* x, int64_t ldx, dpg_dtype x_dtype, const void* residual, int64_t ldr,
@@ -227,9 +258,7 @@ dpg_status dpg_add_layer_norm(const void* x, int64_t ldx, dpg_dtype x_dtype, con
   p.bias = bias;
   p.mean = mean;
   p.rstd = rstd;
-  p.y_bf16 = y_dtype == DPG_BF16;
-  p.branch_bf16 = x_dtype == DPG_BF16;
-  return run_norm(p, sum_dtype == DPG_BF16, true, T, H, eps, stream);
+  return run_norm(p, sum_dtype == DPG_BF16, y_dtype == DPG_BF16, true, x_dtype == DPG_BF16, T, H, eps, stream);
 }
 
 size_t dpg_layer_norm_workspace_size(int64_t T, int64_t H) {
@@ -259,8 +288,7 @@ dpg_status dpg_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_dtype
   p.mean = mean;
   p.rstd = rstd;
   p.weight = weight;
-  p.dy_bf16 = dy_dtype == DPG_BF16;
-  return run_norm_grad(p, x_dtype == DPG_BF16, false, T, H, dweight, dbias, workspace, workspace_bytes, stream);
+  return run_norm_grad(p, x_dtype == DPG_BF16, dy_dtype == DPG_BF16, false, T, H, dweight, dbias, workspace, workspace_bytes, stream);
 }
 
 dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_dtype, const void* sum, int64_t lds,
@@ -292,9 +320,8 @@ dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_d
   p.mean = mean;
   p.rstd = rstd;
   p.weight = weight;
-  p.dy_bf16 = dy_dtype == DPG_BF16;
   p.dx_bf16 = dx_dtype == DPG_BF16;
-  return run_norm_grad(p, sum_dtype == DPG_BF16, true, T, H, dweight, dbias, workspace, workspace_bytes, stream);
+  return run_norm_grad(p, sum_dtype == DPG_BF16, dy_dtype == DPG_BF16, true, T, H, dweight, dbias, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
