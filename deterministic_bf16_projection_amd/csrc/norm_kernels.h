@@ -85,26 +85,38 @@ struct NormPlace {
   }
 };
 
+// columns of wave w of a row
+template <int C>
+__device__ __forceinline__ float row_columns(const NormPlace& q, int waves, int w) {
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) n += min(64, max(0, q.chunks - (c * waves + w) * 64));
+  return 8.f * (float)n;
+}
+
+// sum / count, inverse = 1 / count: the product and its remainder, for a quotient
+// that is exact where there is one (a row of one value has that as its mean),
+// without the ten dependent steps of a division in every row.
+__device__ __forceinline__ float mean_of(float sum, float count, float inverse) {
+  const float q = sum * inverse;
+  return fabsf(q) < __builtin_inff() ? fmaf(fmaf(-q, count, sum), inverse, q) : q;
+}
+
 // A row's mean and sum of squared differences from it.  The waves of a row
 // each take those of their own columns and meet once, in LDS:
 //   mean = sum n_w mean_w / H,   m2 = sum (m2_w + n_w (mean_w - mean)^2)
 template <int C>
-__device__ __forceinline__ void row_statistics(const float (&v)[C][8], const NormPlace& q, int waves,
-                                               float (*shared)[2], float& mean, float& m2) {
+__device__ __forceinline__ void row_statistics(const float (&v)[C][8], const NormPlace& q, int waves, float inv_h,
+                                               float inv_n, float (*shared)[2], float& mean, float& m2) {
   float s = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += v[c][j];
-  const auto columns = [&](int w) {
-    int n = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) n += min(64, max(0, q.chunks - (c * waves + w) * 64));
-    return 8.f * (float)n;
-  };
+  const auto columns = [&](int w) { return row_columns<C>(q, waves, w); };
   const float n = columns(q.wave);
   s = wave_sum(s);
-  float m = n > 0.f ? s / n : 0.f, sq = 0.f;
+  float m = mean_of(s, n, inv_n), sq = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const bool have = (c * waves + q.wave) * 64 + q.lane < q.chunks;
@@ -124,7 +136,7 @@ __device__ __forceinline__ void row_statistics(const float (&v)[C][8], const Nor
     const float(*own)[2] = shared + q.set * waves;
     m = 0.f;
     for (int w = 0; w < waves; ++w) m = fmaf(columns(w), own[w][0], m);
-    m /= 8.f * (float)q.chunks;  // a row of one value has that as its mean
+    m = mean_of(m, 8.f * (float)q.chunks, inv_h);
     sq = 0.f;
     for (int w = 0; w < waves; ++w) {
       const float d = own[w][0] - m;
@@ -178,6 +190,7 @@ __global__ void __launch_bounds__(norm_threads(C)) norm_kernel(NormParams p) {
       load_columns(p.bias, chunk(c), 0.f, b[c]);
     }
   }
+  const float own = row_columns<C>(q, p.waves, q.wave), inv_n = own > 0.f ? 1.f / own : 0.f;
   DropKey key{};
   if (ADD) key = drop_key(p.drop);
   int turn = 0;
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(norm_threads(C)) norm_kernel(NormParams p) {
     float mean, m2;
     // two places in LDS by turns: a wave may write for the next row while
     // others still read, and the barrier of the next row ends their reading
-    row_statistics<C>(v, q, p.waves, shared[turn], mean, m2);
+    row_statistics<C>(v, q, p.waves, p.inv_h, inv_n, shared[turn], mean, m2);
     turn ^= 1;
     const float rstd = 1.f / sqrtf(m2 * p.inv_h + p.eps);
     if (!live) continue;
@@ -283,6 +296,7 @@ __global__ void __launch_bounds__(64 * kNormWaves) norm_dgrad_kernel(NormGradPar
     for (int j = 0; j < 8; ++j) w[c][j] = dw[c][j] = db[c][j] = 0.f;
     if (chunk(c) < q.chunks) load_columns(p.weight, chunk(c), 1.f, w[c]);
   }
+  const float inv_h = 1.f / (float)p.H;
   DropKey key{};
   if (ADD) key = drop_key(p.drop);
   int turn = 0;
@@ -332,8 +346,8 @@ __global__ void __launch_bounds__(64 * kNormWaves) norm_dgrad_kernel(NormGradPar
       }
       turn ^= 1;
     }
-    s1 /= (float)p.H;  // a row of one gradient has that as its mean
-    s2 /= (float)p.H;
+    s1 = mean_of(s1, (float)p.H, inv_h);
+    s2 = mean_of(s2, (float)p.H, inv_h);
     if (!live) continue;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
