@@ -101,6 +101,28 @@ def test_residual_sum(H, x, branch):
         _check("dbias", d.dbias, db, eb)
 
 
+@pytest.mark.parametrize("y", list(TYPES))
+@pytest.mark.parametrize("x", list(TYPES))
+@pytest.mark.parametrize("H", [8, 520, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 12296, 16384])
+def test_many_rows(H, x, y):
+    """Enough rows for the cuts that give each as few waves as hold it; the last
+    rows are no whole round."""
+    T = 1025 + 8 * (H % 3)
+    g = torch.Generator(device="cuda").manual_seed(H)
+    v = torch.randn(T, H, generator=g, device="cuda").mul_(2).add_(0.7).to(TYPES[x])
+    w, b = _affine(torch.Generator().manual_seed(H), H)
+    n = dpg.dpg_layer_norm(v, w, b, eps=EPS, out_dtype=TYPES[y])
+    hw, hb = ref.host(w), ref.host(b)
+    for rows in (slice(0, 9), slice(T // 2, T // 2 + 9), slice(T - 9, T)):
+        wy, wm, wr, ey, em, er = ref.layer_norm(ref.host(v[rows]), hw, hb, EPS)
+        _check("y", n.y[rows], wy, ey, TYPES[y])
+        _check("mean", n.mean[rows], wm, em)
+        _check("rstd", n.rstd[rows], wr, er)
+    few = dpg.dpg_layer_norm(v[:7], w, b, eps=EPS, out_dtype=TYPES[y])  # another cut: as near as both bounds
+    _, _, _, ey, em, _ = ref.layer_norm(ref.host(v[:7]), hw, hb, EPS)
+    assert bool((np.abs(ref.host(few.mean) - ref.host(n.mean[:7])) <= 2 * em + 2 * ref.U * np.abs(ref.host(few.mean))).all())
+
+
 def test_without_dropout_the_sum_is_a_sum():
     g = torch.Generator().manual_seed(2)
     x, r = _randn(g, 33, 264, dtype=BF16), _randn(g, 33, 264)

@@ -223,6 +223,68 @@ def test_no_rows_and_no_channels():
             assert torch.equal(b.dstate, state)
 
 
+def test_packed_rows_of_no_sequence():
+    x = torch.full((300, 16), float("nan"), dtype=BF16, device="cuda")
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = dpg.dpg_recurrence(x, x, offsets=off, carries=True)
+    assert bool((r.h == 0).all()) and r.state.shape == (0, 16)
+    b = dpg.dpg_recurrence_dgrad(x, x, x, r.carries, offsets=off)
+    assert bool((b.dgate == 0).all()) and bool((b.dx == 0).all())
+
+
+def test_offsets_out_of_range_stay_inside():
+    """Values are unspecified; what lies around the outputs stays."""
+    for offsets in ([0, 5, 5000, 7, 90], [0, -3, 40, 1 << 30, 60], [50, 10, 80, 20, 400]):
+        off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        d = _inputs(300, 4, 24, F32, seed=1)
+        whole = torch.full((320, 24), 7.0, device="cuda")
+        last = torch.full((8, 24), 7.0, device="cuda")
+        dpg.dpg_recurrence(d["gate"], d["x"], offsets=off, state=d["state"], out=whole[10:310], state_out=last[2:6])
+        assert bool((whole[:10] == 7).all()) and bool((whole[310:] == 7).all())
+        assert bool((last[:2] == 7).all()) and bool((last[6:] == 7).all())
+
+
+def test_two_streams_at_once():
+    d = [_inputs(2 * 3000, 2, 72, BF16, seed=20 + i) for i in range(2)]
+    want = [_run(x, None, True, (2, 3000, 72)) for x in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(_run(d[i], None, True, (2, 3000, 72)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r, b in got[i]:
+            assert torch.equal(r.h, want[i][0].h) and torch.equal(r.state, want[i][0].state)
+            assert all(torch.equal(x, y) for x, y in zip(b, want[i][1]))
+
+
+def test_captured_with_the_state_in_place():
+    """A graph of a prefill in spans and of generation steps, replayed: each replay
+    starts from the state the one before left."""
+    d = _inputs(2000, 1, 40, BF16, seed=30)
+    gate, x = d["gate"].view(1, 2000, 40), d["x"].view(1, 2000, 40)
+    state = d["state"].clone()
+
+    def both(s):
+        a = dpg.dpg_recurrence(gate, x, state=s, state_out=s)
+        return a.h, dpg.dpg_recurrence(gate[:, :1], x[:, :1], state=s, state_out=s).h
+    both(state.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, step = both(state)
+    state.copy_(d["state"])
+    own = d["state"].clone()
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = both(own)
+        assert torch.equal(h, a) and torch.equal(step, b) and torch.equal(state, own)
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_reruns_give_the_same_bits(packed):
     d = _inputs(4000, 4, 72, BF16, seed=11)
