@@ -21,7 +21,11 @@ constexpr int64_t kMaxRows = (1ll << 31) - 1;
 constexpr int64_t kNormColumns = kNormWaves * 1024;
 struct NormLayout {
   int chunks, waves, sets;  // groups of eight columns of a lane; waves of a row; rows of a workgroup at once
+  int lanes;                // of a row in a wave: below 64, several rows share the wave
+  int threads() const { return lanes < 64 ? lanes * sets : 64 * waves * sets; }
 };
+// Rows of up to 256 columns leave a wave half empty or more: LANES rows to a wave.
+int norm_lanes(int64_t H) { return H <= 64 ? 8 : H <= 128 ? 16 : H <= 256 ? 32 : 64; }
 // Forward.  Few rows, and sums: up to two groups to a lane, weights in
 // registers, so that a row's latency is spread over waves.  Many rows: as few
 // waves to a row as hold it with eight groups to a lane, so that none waits for
@@ -37,6 +41,8 @@ NormLayout norm_layout(int64_t T, int64_t H, bool add) {
   l.waves = (int)((H + 512 * l.chunks - 1) / (512 * l.chunks));
   // workgroups of enough waves for eight to a CU with their weights in LDS
   l.sets = std::max(1, (norm_shares_weights(l.chunks) && H > 4096 ? 8 : 4) / l.waves);
+  l.lanes = norm_lanes(H);
+  l.sets *= 64 / l.lanes;
   return l;
 }
 // workgroups that go through all rows: 2 to 8 to a CU
@@ -49,7 +55,8 @@ NormLayout grad_layout(int64_t H) {
   NormLayout l;
   l.chunks = H <= kNormWaves * 512 ? 1 : 2;
   l.waves = (int)((H + 512 * l.chunks - 1) / (512 * l.chunks));
-  l.sets = kNormWaves / l.waves;
+  l.lanes = norm_lanes(H);
+  l.sets = kNormWaves / l.waves * (64 / l.lanes);
   return l;
 }
 // One workgroup to a CU, and at least two rows of each set where there are so many.
@@ -59,37 +66,40 @@ int64_t grad_blocks(int64_t T, int64_t H) {
   return std::min(kGradBlocks, (T + each - 1) / each);
 }
 
-template <bool X, bool Y, int C>
+template <bool X, bool Y, int C, bool SMALL>
 const void* norm_fn(bool add, bool branch) {
-  if constexpr (norm_shares_weights(C)) return (const void*)&norm_kernel<X, Y, C, false, X>;
-  return !add ? (const void*)&norm_kernel<X, Y, C, false, X>
-              : branch ? (const void*)&norm_kernel<X, Y, C, true, true> : (const void*)&norm_kernel<X, Y, C, true, false>;
+  if constexpr (norm_shares_weights(C)) return (const void*)&norm_kernel<X, Y, C, false, X, SMALL>;
+  return !add ? (const void*)&norm_kernel<X, Y, C, false, X, SMALL>
+              : branch ? (const void*)&norm_kernel<X, Y, C, true, true, SMALL> : (const void*)&norm_kernel<X, Y, C, true, false, SMALL>;
 }
-template <int C>
+template <int C, bool SMALL>
 const void* norm_fn(bool x, bool y, bool add, bool branch) {
-  return x ? (y ? norm_fn<true, true, C>(add, branch) : norm_fn<true, false, C>(add, branch))
-           : (y ? norm_fn<false, true, C>(add, branch) : norm_fn<false, false, C>(add, branch));
+  return x ? (y ? norm_fn<true, true, C, SMALL>(add, branch) : norm_fn<true, false, C, SMALL>(add, branch))
+           : (y ? norm_fn<false, true, C, SMALL>(add, branch) : norm_fn<false, false, C, SMALL>(add, branch));
 }
-const void* norm_fn(int chunks, bool x, bool y, bool add, bool branch) {
-  switch (chunks) {
-    case 1: return norm_fn<1>(x, y, add, branch);
-    case 2: return norm_fn<2>(x, y, add, branch);
-    case 4: return norm_fn<4>(x, y, add, branch);
-    default: return norm_fn<8>(x, y, add, branch);
+const void* norm_fn(const NormLayout& l, bool x, bool y, bool add, bool branch) {
+  if (l.lanes < 64) return norm_fn<1, true>(x, y, add, branch);
+  switch (l.chunks) {
+    case 1: return norm_fn<1, false>(x, y, add, branch);
+    case 2: return norm_fn<2, false>(x, y, add, branch);
+    case 4: return norm_fn<4, false>(x, y, add, branch);
+    default: return norm_fn<8, false>(x, y, add, branch);
   }
+}
+template <bool X, bool DY, int C, bool SMALL>
+const void* norm_dgrad_fn(bool add) {
+  return add ? (const void*)&norm_dgrad_kernel<X, DY, C, true, SMALL> : (const void*)&norm_dgrad_kernel<X, DY, C, false, SMALL>;
+}
+template <bool X, bool DY>
+const void* norm_dgrad_fn(const NormLayout& l, bool add) {
+  if (l.lanes < 64) return norm_dgrad_fn<X, DY, 1, true>(add);
+  return l.chunks == 1 ? norm_dgrad_fn<X, DY, 1, false>(add) : norm_dgrad_fn<X, DY, 2, false>(add);
 }
 template <bool X, bool Y>
 const void* dropout_fn(bool add, bool past) {
   if (add) return past ? (const void*)&dropout_kernel<X, Y, true, true> : (const void*)&dropout_kernel<X, Y, true, false>;
   return past ? (const void*)&dropout_kernel<X, Y, false, true> : (const void*)&dropout_kernel<X, Y, false, false>;
 }
-template <bool X, bool DY>
-const void* norm_dgrad_fn(int chunks, bool add) {
-  if (add)
-    return chunks == 1 ? (const void*)&norm_dgrad_kernel<X, DY, 1, true> : (const void*)&norm_dgrad_kernel<X, DY, 2, true>;
-  return chunks == 1 ? (const void*)&norm_dgrad_kernel<X, DY, 1, false> : (const void*)&norm_dgrad_kernel<X, DY, 2, false>;
-}
-
 dpg_status check_norm(int64_t T, int64_t H) {
   if (T < 0 || H < 0) return DPG_ERR_INVALID_ARG;
   if (T > kMaxRows || H > kNormColumns) return DPG_ERR_UNSUPPORTED;
@@ -128,12 +138,13 @@ dpg_status run_norm(NormParams& p, bool x_bf16, bool y_bf16, bool add, bool bran
   p.H = (int)H;
   p.waves = l.waves;
   p.groups = l.sets;
+  p.lanes = l.lanes;
   p.inv_h = 1.f / (float)H;
   p.eps = (float)eps;
-  const void* fn = norm_fn(l.chunks, x_bf16, y_bf16, add, branch_bf16);
+  const void* fn = norm_fn(l, x_bf16, y_bf16, add, branch_bf16);
   const size_t lds = norm_shares_weights(l.chunks) ? (size_t)H * 2 * sizeof(float) : 0;
   void* args[] = {&p};
-  return launch(fn, std::min<int64_t>((T + l.sets - 1) / l.sets, norm_grid(l)), 64 * l.waves * l.sets, lds, args, stream);
+  return launch(fn, std::min<int64_t>((T + l.sets - 1) / l.sets, norm_grid(l)), l.threads(), lds, args, stream);
 }
 
 dpg_status run_norm_grad(NormGradParams& p, bool x_bf16, bool dy_bf16, bool add, int64_t T, int64_t H, float* dweight,
@@ -149,14 +160,15 @@ dpg_status run_norm_grad(NormGradParams& p, bool x_bf16, bool dy_bf16, bool add,
   p.H = (int)H;
   p.waves = l.waves;
   p.groups = l.sets;
+  p.lanes = l.lanes;
   int blocks = 0;
   if (T > 0) {
     blocks = (int)grad_blocks(T, H);
-    const void* fn = x_bf16 ? (dy_bf16 ? norm_dgrad_fn<true, true>(l.chunks, add) : norm_dgrad_fn<true, false>(l.chunks, add))
-                            : (dy_bf16 ? norm_dgrad_fn<false, true>(l.chunks, add) : norm_dgrad_fn<false, false>(l.chunks, add));
+    const void* fn = x_bf16 ? (dy_bf16 ? norm_dgrad_fn<true, true>(l, add) : norm_dgrad_fn<true, false>(l, add))
+                            : (dy_bf16 ? norm_dgrad_fn<false, true>(l, add) : norm_dgrad_fn<false, false>(l, add));
     const size_t lds = sums && l.sets > 1 ? (size_t)l.sets * H * sizeof(float) : 0;
     void* args[] = {&p};
-    const dpg_status st = launch(fn, blocks, 64 * l.waves * l.sets, lds, args, stream);
+    const dpg_status st = launch(fn, blocks, l.threads(), lds, args, stream);
     if (st != DPG_OK) return st;
   }
   if (!sums) return DPG_OK;

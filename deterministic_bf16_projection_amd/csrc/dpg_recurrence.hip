@@ -46,8 +46,8 @@ dpg_status rec_plan(int64_t S, int64_t R, int64_t D, bool packed, RecPlan& g) {
   g.blocks = (D + kRecChannels - 1) / kRecChannels;
   const int64_t have = g.axes * g.blocks;
   g.spans = 1;
-  if (have * 2 <= kRecFull && g.tiles > 4)
-    g.spans = std::min(kRecFull / have, g.tiles / 2);
+  if (have * 2 <= kRecFull && g.tiles > 2)
+    g.spans = std::min(kRecFull / have, g.tiles);
   g.span_tiles = (g.tiles + g.spans - 1) / g.spans;
   g.spans = (g.tiles + g.span_tiles - 1) / g.span_tiles;
   if (g.axes * g.spans * g.blocks >= (1ll << 22)) return DPG_ERR_UNSUPPORTED;

@@ -12,8 +12,8 @@
 // Every kernel reads its rows once and keeps them in registers: bound by
 // memory.  `waves` waves share a row, each lane holding C groups of eight
 // columns, and go from row to row with the weights in registers, the next row's
-// loads in flight.  A workgroup has `groups` sets of such waves.  Statistics and
-// sums are FP32.
+// loads in flight.  A workgroup has `groups` sets of such waves (or of lanes,
+// where rows are short).  Statistics and sums are FP32.
 #pragma once
 #include "dropout_kernels.h"
 
@@ -67,27 +67,43 @@ struct NormParams {
   float* mean;
   float* rstd;
   int64_t T;
-  int H, waves, groups;
+  int H, waves, groups, lanes;
   float inv_h, eps;
   DropParams drop;
 };
 
 // A lane's place: the wave among those of its row, and its row's place among the
-// workgroup's.
+// workgroup's.  SMALL: `lanes` (8, 16 or 32) lanes hold a row, and a wave several
+// rows; else a row has whole waves.
+template <bool SMALL>
 struct NormPlace {
-  int lane, id, wave, set, chunks;  // chunks: groups of eight columns of a row
-  __device__ __forceinline__ NormPlace(int waves, int H) {
-    lane = threadIdx.x & 63;
-    id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    set = id / waves;
-    wave = id - set * waves;
+  int lane, id, wave, set, chunks, lanes;  // chunks: groups of eight columns of a row
+  __device__ __forceinline__ NormPlace(int waves, int H, int lanes_of_row) {
     chunks = H >> 3;
+    if constexpr (SMALL) {
+      lanes = lanes_of_row;
+      lane = threadIdx.x & (lanes - 1);
+      set = threadIdx.x / (unsigned)lanes;
+      id = wave = 0;
+    } else {
+      lanes = 64;
+      lane = threadIdx.x & 63;
+      id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      set = id / waves;
+      wave = id - set * waves;
+    }
+  }
+  // over the lanes of one row (of one of its waves)
+  __device__ __forceinline__ float sum(float v) const {
+    if constexpr (!SMALL) return wave_sum(v);
+    for (int m = lanes >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    return v;
   }
 };
 
 // columns of wave w of a row
-template <int C>
-__device__ __forceinline__ float row_columns(const NormPlace& q, int waves, int w) {
+template <int C, bool SMALL>
+__device__ __forceinline__ float row_columns(const NormPlace<SMALL>& q, int waves, int w) {
   int n = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) n += min(64, max(0, q.chunks - (c * waves + w) * 64));
@@ -105,17 +121,17 @@ __device__ __forceinline__ float mean_of(float sum, float count, float inverse) 
 // A row's mean and sum of squared differences from it.  The waves of a row
 // each take those of their own columns and meet once, in LDS:
 //   mean = sum n_w mean_w / H,   m2 = sum (m2_w + n_w (mean_w - mean)^2)
-template <int C>
-__device__ __forceinline__ void row_statistics(const float (&v)[C][8], const NormPlace& q, int waves, float inv_h,
+template <int C, bool SMALL>
+__device__ __forceinline__ void row_statistics(const float (&v)[C][8], const NormPlace<SMALL>& q, int waves, float inv_h,
                                                float inv_n, float (*shared)[2], float& mean, float& m2) {
   float s = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += v[c][j];
-  const auto columns = [&](int w) { return row_columns<C>(q, waves, w); };
+  const auto columns = [&](int w) { return row_columns<C, SMALL>(q, waves, w); };
   const float n = columns(q.wave);
-  s = wave_sum(s);
+  s = q.sum(s);
   float m = mean_of(s, n, inv_n), sq = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -126,7 +142,7 @@ __device__ __forceinline__ void row_statistics(const float (&v)[C][8], const Nor
       sq = fmaf(d, d, sq);
     }
   }
-  sq = wave_sum(sq);
+  sq = q.sum(sq);
   if (waves > 1) {
     if (q.lane == 0) {
       shared[q.id][0] = m;
@@ -147,12 +163,12 @@ __device__ __forceinline__ void row_statistics(const float (&v)[C][8], const Nor
   m2 = sq;
 }
 
-template <bool X_BF16, bool Y_BF16, int C, bool ADD, bool BRANCH_BF16>
+template <bool X_BF16, bool Y_BF16, int C, bool ADD, bool BRANCH_BF16, bool SMALL>
 __global__ void __launch_bounds__(norm_threads(C)) norm_kernel(NormParams p) {
   constexpr bool SHARED = norm_shares_weights(C);
   __shared__ float shared[2][kNormWaves][2];
   extern __shared__ __attribute__((aligned(16))) float columns[];  // SHARED: weight and bias, see column_place
-  const NormPlace q(p.waves, p.H);
+  const NormPlace<SMALL> q(p.waves, p.H, p.lanes);
   const int64_t stride = (int64_t)gridDim.x * p.groups;
   int64_t first = (int64_t)blockIdx.x * p.groups;  // of the workgroup's rows
   const auto chunk = [&](int c) { return (c * p.waves + q.wave) * 64 + q.lane; };
@@ -190,7 +206,7 @@ __global__ void __launch_bounds__(norm_threads(C)) norm_kernel(NormParams p) {
       load_columns(p.bias, chunk(c), 0.f, b[c]);
     }
   }
-  const float own = row_columns<C>(q, p.waves, q.wave), inv_n = own > 0.f ? 1.f / own : 0.f;
+  const float own = row_columns<C, SMALL>(q, p.waves, q.wave), inv_n = own > 0.f ? 1.f / own : 0.f;
   DropKey key{};
   if (ADD) key = drop_key(p.drop);
   int turn = 0;
@@ -221,7 +237,7 @@ __global__ void __launch_bounds__(norm_threads(C)) norm_kernel(NormParams p) {
     float mean, m2;
     // two places in LDS by turns: a wave may write for the next row while
     // others still read, and the barrier of the next row ends their reading
-    row_statistics<C>(v, q, p.waves, p.inv_h, inv_n, shared[turn], mean, m2);
+    row_statistics<C, SMALL>(v, q, p.waves, p.inv_h, inv_n, shared[turn], mean, m2);
     turn ^= 1;
     const float rstd = 1.f / sqrtf(m2 * p.inv_h + p.eps);
     if (!live) continue;
@@ -256,7 +272,7 @@ struct NormGradParams {
   const float* weight;  // or null
   float* partial;       // [blocks, 2, H]: sums of dy n and of dy, or null
   int64_t T;
-  int H, waves, groups;
+  int H, waves, groups, lanes;
   bool dx_bf16;         // sum
   DropParams drop;
 };
@@ -264,11 +280,11 @@ struct NormGradParams {
 // Each wave adds up dy n and dy over its rows in registers; a workgroup's sets
 // of waves meet in LDS (groups * H floats), set after set, and its sums are one
 // row of `partial`.
-template <bool X_BF16, bool DY_BF16, int C, bool ADD>
+template <bool X_BF16, bool DY_BF16, int C, bool ADD, bool SMALL>
 __global__ void __launch_bounds__(64 * kNormWaves) norm_dgrad_kernel(NormGradParams p) {
   __shared__ float shared[2][kNormWaves][2];
   extern __shared__ __attribute__((aligned(16))) float sums[];
-  const NormPlace q(p.waves, p.H);
+  const NormPlace<SMALL> q(p.waves, p.H, p.lanes);
   const int64_t stride = (int64_t)gridDim.x * p.groups;
   const auto chunk = [&](int c) { return (c * p.waves + q.wave) * 64 + q.lane; };
   float w[C][8], dw[C][8], db[C][8];
@@ -330,8 +346,8 @@ __global__ void __launch_bounds__(64 * kNormWaves) norm_dgrad_kernel(NormGradPar
       }
     }
     fetch(t + stride);
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
+    s1 = q.sum(s1);
+    s2 = q.sum(s2);
     if (p.waves > 1) {
       if (q.lane == 0) {
         shared[turn][q.id][0] = s1;

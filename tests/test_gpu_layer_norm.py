@@ -33,7 +33,7 @@ def _affine(g, H):
 
 
 # each number of waves to a row and groups to a lane, at its ends
-WIDTHS = [8, 16, 504, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 6144, 6152, 8192, 8200, 12288, 12296, 16384]
+WIDTHS = [8, 16, 64, 72, 128, 136, 256, 264, 504, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 6144, 6152, 8192, 8200, 12288, 12296, 16384]
 
 
 @pytest.mark.parametrize("y", list(TYPES))
@@ -64,7 +64,7 @@ def test_forward_and_gradient(H, x, y):
 
 @pytest.mark.parametrize("branch", list(TYPES))
 @pytest.mark.parametrize("x", list(TYPES))
-@pytest.mark.parametrize("H", [8, 520, 1024, 2048, 4096, 6144, 8192, 12288, 16384])
+@pytest.mark.parametrize("H", [8, 56, 120, 256, 520, 1024, 2048, 4096, 6144, 8192, 12288, 16384])
 def test_residual_sum(H, x, branch):
     T, p, seed = (29 if H < 4096 else 7), 0.3, 0x123456789ABCDEF0 + H
     g = torch.Generator().manual_seed(H + 1)
@@ -103,7 +103,7 @@ def test_residual_sum(H, x, branch):
 
 @pytest.mark.parametrize("y", list(TYPES))
 @pytest.mark.parametrize("x", list(TYPES))
-@pytest.mark.parametrize("H", [8, 520, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 12296, 16384])
+@pytest.mark.parametrize("H", [8, 64, 104, 248, 520, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 12296, 16384])
 def test_many_rows(H, x, y):
     """Enough rows for the cuts that give each as few waves as hold it; the last
     rows are no whole round."""
@@ -175,7 +175,7 @@ def test_constant_rows_and_strange_values():
 
 
 @pytest.mark.parametrize("T", [1, 2, 3, 5, 8, 9, 511, 513, 4095, 4097, 5000])
-@pytest.mark.parametrize("H", [40, 1032])
+@pytest.mark.parametrize("H", [40, 128, 248, 1032])
 def test_row_counts(T, H):
     """Whole numbers: dbias is exact, whatever the cut over workgroups."""
     g = torch.Generator().manual_seed(T)
