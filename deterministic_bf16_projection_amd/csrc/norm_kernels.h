@@ -14,6 +14,11 @@
 // columns, and go from row to row with the weights in registers, the next row's
 // loads in flight.  A workgroup has `groups` sets of such waves (or of lanes,
 // where rows are short).  Statistics and sums are FP32.
+//
+// 16384 rows of 4096 columns, BF16: forward 47-52 us (5.2-5.7 TB/s), gradient 79 us
+// (73 us and 5.6 TB/s for the rows, 5 us for the weight gradient's last sums).
+// A sum of 8192 such rows, FP32 stream and BF16 branch: 78 us (5.2 TB/s); its
+// gradient of 5003 x 5120 82 us (5.0).  Non-temporal accesses are level.
 #pragma once
 #include "dropout_kernels.h"
 

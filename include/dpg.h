@@ -559,7 +559,7 @@ dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_d
  * that depends on the sizes alone.  Workspace: dpg_recurrence_workspace_size
  * bytes, 16-byte aligned; packed = whether offsets are given.  State matrices
  * and carries are 16-byte aligned.  R at most 2^30, S and D at most 2^24
- * (DPG_ERR_UNSUPPORTED beyond, and for launches of more than 2^23 workgroups).
+ * (DPG_ERR_UNSUPPORTED beyond, and for launches of 2^22 workgroups or more).
  */
 size_t dpg_recurrence_workspace_size(int64_t S, int64_t R, int64_t D, dpg_dtype dtype, int packed);
 size_t dpg_recurrence_carries_size(int64_t S, int64_t R, int64_t D, dpg_dtype dtype, int packed);
