@@ -94,6 +94,9 @@ __device__ __forceinline__ Raw2<BF16> pack2(const f32x2& v) {
 __device__ float mul_zero_wins(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
 __device__ __forceinline__ float weighted(float a, float b) { return mul_zero_wins(a, b); }
 __device__ __forceinline__ float carry_on(float a, float c, float b) { return weighted(a, c) + b; }
+// v, and NaN where the weight f (0 to 1) is, which a term of 0 would hide in
+// weighted() and the minimum in 1 - f
+__device__ __forceinline__ float or_nan(float f, float v) { return fmaf(f, 0.f, v); }
 // a product of weights: 0 exactly where the least of them is, else at least the
 // smallest normal number
 __device__ __forceinline__ float held(float product, float least) { return fmaxf(product, fminf(least, 0x1p-126f)); }
@@ -316,7 +319,7 @@ __device__ __forceinline__ void rec_inputs(const RecParams& p, const RecPlace& q
       float fk, rest;
       gate_weights<BF16>(g[k], fk, rest);
       f[u][k] = fk;
-      b[u][k] = COUPLED ? weighted(rest, v[k]) : v[k];
+      b[u][k] = or_nan(fk, COUPLED ? weighted(rest, v[k]) : v[k]);
     }
   }
   if (e.plain) return;
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecParams p) {
     for (int j = 0; j < 8; ++j) {
       float f, rest;
       gate_weights<BF16>(g[j], f, rest);
-      h[j] = carry_on(f, c[j >> 2][j & 3], COUPLED ? weighted(rest, x[j]) : x[j]);
+      h[j] = carry_on(f, c[j >> 2][j & 3], or_nan(f, COUPLED ? weighted(rest, x[j]) : x[j]));
     }
     store8<BF16>(p.h, row, group, h);
     if (p.state_out) {
@@ -529,7 +532,7 @@ __device__ __forceinline__ void rec_compose_back(const RecParams& p, const RecPl
     for (int k = 0; k < 2; ++k) {
       A[k] *= fu[k];
       least[k] = fminf(least[k], fu[k]);
-      Q[k] = weighted(fu[k], dh[k] + Q[k]);
+      Q[k] = weighted(fu[k], or_nan(fu[k], dh[k] + Q[k]));
     }
   }
 #pragma unroll
@@ -549,7 +552,7 @@ __device__ __forceinline__ f32x2 rec_states(const RecParams& p, const RecPlace& 
     if (e.start >> u & 1) h = rec_state(p.state, p, e, q, row, u);
     before[u] = h;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) h[k] = carry_on(f[u][k], h[k], COUPLED ? weighted(rest[u][k], v[k]) : v[k]);
+    for (int k = 0; k < 2; ++k) h[k] = carry_on(f[u][k], h[k], or_nan(f[u][k], COUPLED ? weighted(rest[u][k], v[k]) : v[k]));
   }
   return h;
 }
@@ -623,8 +626,8 @@ __global__ void __launch_bounds__(kRecGradThreads, 2) recurrence_dgrad_kernel(Re
         f32x2 out_x, out_g;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float r = du[k] + c[k];
-          out_x[k] = COUPLED ? weighted(rest[u][k], r) : r;
+          const float plain = du[k] + c[k], r = or_nan(f[u][k], plain);
+          out_x[k] = COUPLED ? weighted(rest[u][k], r) : plain;
           out_g[k] = weighted(f[u][k] * rest[u][k], r * (COUPLED ? before[u][k] - xu[k] : before[u][k]));
           c[k] = weighted(f[u][k], r);
         }

@@ -152,6 +152,35 @@ def test_weights_of_zero_leave_their_terms_out(coupled, dtype):
         assert bool((np.abs(got - want[name])[fine] <= limit[fine]).all()), name
 
 
+@pytest.mark.parametrize("T", [1, 700, 40], ids=["steps", "spans", "short"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("coupled", [True, False], ids=["coupled", "free"])
+@pytest.mark.parametrize("state", [True, False], ids=["state", "zeros"])
+def test_a_gate_of_nan_is_one_of_its_row_on(state, coupled, dtype, T):
+    """At places of a run and of a tile, and next to inputs, states and gradients
+    of 0, which hide no NaN: outputs from the row on, gradients up to it."""
+    B, D = 3, 64
+    d = _inputs(B * T, B, D, dtype, seed=12, state=state)
+    gate, x, dh = (d[k].view(B, T, D) for k in ("gate", "x", "dh"))
+    for i, t in enumerate([0, 1, 7, 8, 39, 63, 64, 65, 127, 128, 300, 512, T - 1]):
+        if t >= T:
+            continue
+        for k in range(4):
+            c = 4 * i + k
+            gate[1, t, c] = float("nan")
+            if k & 1:
+                x[1, :t + 1, c] = 0
+                if state:
+                    d["state"][1, c] = 0
+            if k & 2:
+                dh[1, t:, c] = 0
+                if state:
+                    d["dstate"][1, c] = 0
+    offsets = [0, T, 2 * T, 3 * T]
+    _compare(d, offsets, coupled, *_run(d, offsets, coupled, (B, T, D)))
+    _compare(d, offsets, coupled, *_run(d, offsets, coupled))
+
+
 def test_an_infinite_state_outlives_products_that_underflow():
     """900 steps of f = e^-2 / (1 + e^-2): the product is 10^-830, the state stays
     infinite."""
