@@ -260,9 +260,16 @@ class _LayerNorm(torch.autograd.Function):
                 d.dbias if need[2] else None, None, None)
 
 
+def _same_shape(x, residual):
+    # the matrices that the library sees could still agree, the gradients' shapes not
+    if residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+
+
 class _AddLayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, p, seed, step, out_dtype):
+        _same_shape(x, residual)
         n = dpg_add_layer_norm(_matrix(x), _matrix(residual), weight, bias, eps=eps, p=p, seed=seed, step=step,
                                out_dtype=out_dtype)
         total = n.sum.view(x.shape)
@@ -294,6 +301,8 @@ class _AddLayerNorm(torch.autograd.Function):
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, seed, step, residual):
+        if residual is not None:
+            _same_shape(x, residual)
         ctx.save_for_backward(step)
         ctx.drop, ctx.x_dtype = (p, seed), x.dtype
         y = dpg_dropout(_matrix(x), p, seed, step=step, residual=None if residual is None else _matrix(residual))

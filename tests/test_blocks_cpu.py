@@ -185,3 +185,13 @@ def test_layer_norm_reference_against_differences():
     dx, dw, db, *_ = ref.layer_norm_dgrad(dy, x, mean, rstd, w)
     for at, grad in ((x, dx), (w, dw), (b, db)):
         assert np.abs(_difference(value, at, 2.0 ** -17) - grad).max() < 1e-8
+
+
+def test_autograd_refuses_a_residual_of_another_shape():
+    """As matrices both have 8 rows."""
+    from deterministic_bf16_projection_amd import autograd
+    x, residual = torch.zeros(2, 4, 8), torch.zeros(8, 8)
+    with pytest.raises(ValueError, match=r"residual has shape \(8, 8\), x \(2, 4, 8\)"):
+        autograd.add_layer_norm(x, residual)
+    with pytest.raises(ValueError, match=r"residual has shape \(8, 8\), x \(2, 4, 8\)"):
+        autograd.dropout(x, 0.1, 1, residual=residual)
