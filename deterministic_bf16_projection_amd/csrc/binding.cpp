@@ -1,10 +1,9 @@
 // Python module _binding: the entry points of include/dpg.h for expert layers and
 // what stands between a block's projections, for torch tensors.  It checks the
-// arguments, allocates the outputs a caller does
-// not give, and launches on the current stream of the tensors' device; no
-// arithmetic.  Compiled, because the same work through ctypes costs about 10 us
-// a call, and 90 us for an optimizer step over 48 tensors, where the kernels of
-// one token take 2 to 6 us.
+// arguments, allocates the outputs a caller does not give, and launches on the
+// current stream of the tensors' device; no arithmetic.  Compiled, because the
+// same work through ctypes costs about 10 us a call, and 90 us for an optimizer
+// step over 48 tensors, where the kernels of one token take 2 to 6 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
