@@ -544,7 +544,7 @@ dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_d
  * carries    : FP32, dpg_recurrence_carries_size bytes, for the gradient; NULL:
  *              not wanted
  * A weight that is exactly 0 leaves its term out whatever the term is, so a
- * gate of -infinity (any below about -88 counts as one) forgets the state, and
+ * gate of -infinity (any below about -87 counts as one) forgets the state, and
  * one of +infinity with `coupled` passes over the input.  A gate that is NaN
  * makes h NaN from its row on, until a weight of 0.
  *
