@@ -14,7 +14,9 @@
 // (A, H) meet in LDS, every wave finds the state before its run, and then each
 // row's, from values that stayed in registers: the rows are read once.  A is
 // zero only if some f is: products that underflow are held at the smallest
-// number, so that an infinite state stays infinite.
+// number, 2^-149, so that an infinite state stays infinite.  Below the normal
+// numbers each multiplication of A is off by up to that: a finite state c that
+// passes whole runs, by |c| 2^-149 for every row of them.
 //
 // Rows are grouped in axes, each a whole sequence or several short ones; a
 // sequence's first row takes f = 0 there and the initial state into its input.
@@ -97,9 +99,9 @@ __device__ __forceinline__ float carry_on(float a, float c, float b) { return we
 // v, and NaN where the weight f (0 to 1) is, which a term of 0 would hide in
 // weighted() and the minimum in 1 - f
 __device__ __forceinline__ float or_nan(float f, float v) { return fmaf(f, 0.f, v); }
-// a product of weights: 0 exactly where the least of them is, else at least the
-// smallest normal number
-__device__ __forceinline__ float held(float product, float least) { return fmaxf(product, fminf(least, 0x1p-126f)); }
+// a product of weights: 0 exactly where the least of them is, else at least 2^-149,
+// the smallest number above 0, which is no more than a product's own rounding
+__device__ __forceinline__ float held(float product, float least) { return fmaxf(product, fminf(least, 0x1p-149f)); }
 // two runs, the first's values first
 __device__ __forceinline__ f32x2 rec_carry(const f32x2& A, const f32x2& c, const f32x2& H) {
   return f32x2{carry_on(A[0], c[0], H[0]), carry_on(A[1], c[1], H[1])};

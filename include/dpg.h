@@ -556,6 +556,9 @@ dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_d
  * and into dstate_out (or NULL), not dstate itself, f r of each first row (an
  * empty sequence's is its dstate).
  *
+ * A state passes several rows at once by the product of their f in FP32, which
+ * below 2^-126 is off by up to 2^-149 for each row: of a large state c, up to
+ * |c| 2^-149 a row may be left where rows one by one would leave less.
  * The states between carries are recomputed in FP32.  Sums run in a fixed order
  * that depends on the sizes alone.  Workspace: dpg_recurrence_workspace_size
  * bytes, 16-byte aligned; packed = whether offsets are given.  State matrices
