@@ -58,10 +58,16 @@ def resolve_deterministic(deterministic):
     return False
 
 
+def _packed(t):
+    """t itself where it is contiguous and starts at a multiple of 16 bytes, as the
+    library takes it, else a copy: a gradient may be a view of a larger one."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _rows(t):
     """[..., C] as a contiguous [R, C] view (the library takes unit column stride)."""
-    t2 = t.reshape(-1, t.shape[-1])
-    return t2 if t2.is_contiguous() else t2.contiguous()
+    return _packed(t.reshape(-1, t.shape[-1]))
 
 
 class _Projection(torch.autograd.Function):
@@ -241,10 +247,21 @@ def combine(ys, r):
     return _Combine.apply(ys, r.weights, r.positions, r.offsets)
 
 
+def _aligned(t, pitch):
+    """Whether t and its rows, `pitch` elements apart, start at multiples of 16 bytes."""
+    return t.data_ptr() % 16 == 0 and pitch * t.element_size() % 16 == 0
+
+
+def _operand(t):
+    """_matrix(t), copied where its rows are not aligned."""
+    t2 = _matrix(t)
+    return t2 if _aligned(t2, t2.stride(0) if t2.shape[0] > 1 else 0) else t2.clone(memory_format=torch.contiguous_format)
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, out_dtype):
-        matrix = _matrix(x)
+        matrix = _operand(x)
         n = dpg_layer_norm(matrix, weight, bias, eps=eps, out_dtype=out_dtype)
         ctx.save_for_backward(matrix, weight, n.mean, n.rstd)
         ctx.shape = x.shape
@@ -270,7 +287,7 @@ class _AddLayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, p, seed, step, out_dtype):
         _same_shape(x, residual)
-        n = dpg_add_layer_norm(_matrix(x), _matrix(residual), weight, bias, eps=eps, p=p, seed=seed, step=step,
+        n = dpg_add_layer_norm(_operand(x), _operand(residual), weight, bias, eps=eps, p=p, seed=seed, step=step,
                                out_dtype=out_dtype)
         total = n.sum.view(x.shape)
         # the step is saved too: counting it up before the backward pass, which
@@ -305,7 +322,7 @@ class _Dropout(torch.autograd.Function):
             _same_shape(x, residual)
         ctx.save_for_backward(step)
         ctx.drop, ctx.x_dtype = (p, seed), x.dtype
-        y = dpg_dropout(_matrix(x), p, seed, step=step, residual=None if residual is None else _matrix(residual))
+        y = dpg_dropout(_operand(x), p, seed, step=step, residual=None if residual is None else _operand(residual))
         return y.view(x.shape)
 
     @staticmethod
@@ -319,13 +336,15 @@ class _Dropout(torch.autograd.Function):
 
 
 def _sequences(t):
-    """t itself where all its rows are one stride apart, else a copy."""
+    """t itself where all its rows are aligned and one stride apart, else a copy."""
     if t.dim() == 2:
-        return _matrix(t)
+        return _operand(t)
     b, n, d = t.shape
     last = d <= 1 or t.stride(2) == 1
     even = n <= 1 or (t.stride(1) >= d and (b <= 1 or t.stride(0) == n * t.stride(1)))
-    return t if last and even and (n > 1 or b <= 1 or t.stride(0) >= d) else t.contiguous()
+    taken = last and even and (n > 1 or b <= 1 or t.stride(0) >= d)
+    taken = taken and _aligned(t, t.stride(1) if n > 1 else t.stride(0) if b > 1 else 0)
+    return t if taken else t.clone(memory_format=torch.contiguous_format)
 
 
 class _Recurrence(torch.autograd.Function):
@@ -346,7 +365,7 @@ class _Recurrence(torch.autograd.Function):
             return (None,) * 5
         dh = torch.zeros_like(x) if dh is None else _sequences(dh)
         d = dpg_recurrence_dgrad(dh, gate, x, carries, offsets=offsets, state=state,
-                                 dstate=None if dstate is None else dstate.contiguous(), coupled=ctx.coupled)
+                                 dstate=None if dstate is None else _packed(dstate), coupled=ctx.coupled)
         return d.dgate, d.dx, None, d.dstate, None
 
 
