@@ -283,6 +283,12 @@ def _same_shape(x, residual):
         raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
 
 
+def _mask_step(p, step):
+    """The step that the backward pass needs: saved, so that counting it up before
+    then is an error that its version shows; none where nothing is left out."""
+    return step if p > 0 else None
+
+
 class _AddLayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, p, seed, step, out_dtype):
@@ -290,9 +296,7 @@ class _AddLayerNorm(torch.autograd.Function):
         n = dpg_add_layer_norm(_operand(x), _operand(residual), weight, bias, eps=eps, p=p, seed=seed, step=step,
                                out_dtype=out_dtype)
         total = n.sum.view(x.shape)
-        # the step is saved too: counting it up before the backward pass, which
-        # needs the same mask, is an error that its version shows
-        ctx.save_for_backward(total, weight, n.mean, n.rstd, step)
+        ctx.save_for_backward(total, weight, n.mean, n.rstd, _mask_step(p, step))
         ctx.drop, ctx.x_dtype = (p, seed), x.dtype
         ctx.set_materialize_grads(False)
         return n.y.view(x.shape), total
@@ -320,7 +324,7 @@ class _Dropout(torch.autograd.Function):
     def forward(ctx, x, p, seed, step, residual):
         if residual is not None:
             _same_shape(x, residual)
-        ctx.save_for_backward(step)
+        ctx.save_for_backward(_mask_step(p, step))
         ctx.drop, ctx.x_dtype = (p, seed), x.dtype
         y = dpg_dropout(_operand(x), p, seed, step=step, residual=None if residual is None else _operand(residual))
         return y.view(x.shape)
