@@ -70,9 +70,10 @@ int64_t grad_blocks(int64_t T, int64_t H) {
 
 template <bool X, bool Y, int C, bool SMALL>
 const void* norm_fn(bool add, bool branch) {
-  if constexpr (norm_shares_weights(C)) return (const void*)&norm_kernel<X, Y, C, false, X, SMALL>;
-  return !add ? (const void*)&norm_kernel<X, Y, C, false, X, SMALL>
-              : branch ? (const void*)&norm_kernel<X, Y, C, true, true, SMALL> : (const void*)&norm_kernel<X, Y, C, true, false, SMALL>;
+  if constexpr (!norm_shares_weights(C)) {  // sums have up to two groups to a lane
+    if (add) return branch ? (const void*)&norm_kernel<X, Y, C, true, true, SMALL> : (const void*)&norm_kernel<X, Y, C, true, false, SMALL>;
+  }
+  return (const void*)&norm_kernel<X, Y, C, false, X, SMALL>;
 }
 template <int C, bool SMALL>
 const void* norm_fn(bool x, bool y, bool add, bool branch) {
