@@ -32,7 +32,10 @@ int norm_lanes(int64_t H) { return H <= 64 ? 8 : H <= 128 ? 16 : H <= 256 ? 32 :
 // registers, so that a row's latency is spread over waves.  Many rows: as few
 // waves to a row as hold it with eight groups to a lane, so that none waits for
 // others (16384 rows of 4096 columns, BF16: one wave 47.8 us, four 52, eight 62;
-// sums of 8192 rows, FP32 and BF16: two waves 81 us, four 78).
+// sums of 8192 rows, FP32 and BF16: two waves 81 us, four 78).  Near the border,
+// BF16, us, many rows' cut and few rows': 1024 rows of 4096 columns 7.3 and 6.5, of
+// 16384 columns 21.3 and 20.7; 2048 rows of 8192 columns 19.0 and 16.3, of 16384
+// 34 and 46; 4096 rows of 4096 columns 14.2 and 14.6, of 8192 31.4 and 32.0.
 constexpr int64_t kNormManyRows = 1024;
 NormLayout norm_layout(int64_t T, int64_t H, bool add) {
   NormLayout l;

@@ -68,8 +68,8 @@ struct DropoutParams {
 
 // 2^lanes_log2 threads to a row.  Rows without gaps come as rows of 512 groups,
 // whatever the tensor's own: two groups to a thread.  Bound by memory: 16384 rows
-// of 12288 BF16 columns in 131 us, 6.1 TB/s (146 through the caches and with one
-// group to a thread; 136 and 160 past them with four or eight times as many).
+// of 12288 BF16 columns in 127 to 131 us, 6.2 TB/s (146 through the caches and with
+// one group to a thread; 136 and 160 past them with four or eight times as many).
 template <bool BF16_IN, bool BF16_OUT, bool ADD, bool NT>
 __global__ void __launch_bounds__(256) dropout_kernel(DropoutParams p) {
   const int lanes = 1 << p.lanes_log2, lane = threadIdx.x & (lanes - 1);

@@ -11,14 +11,17 @@
 //
 // Every kernel reads its rows once and keeps them in registers: bound by
 // memory.  `waves` waves share a row, each lane holding C groups of eight
-// columns, and go from row to row with the weights in registers, the next row's
-// loads in flight.  A workgroup has `groups` sets of such waves (or of lanes,
-// where rows are short).  Statistics and sums are FP32.
+// columns, and go from row to row with the next row's loads in flight (but the
+// gradient's dsum) and the weights in registers; forward with more than two
+// groups to a lane, in LDS.  A workgroup has `groups` sets of such waves (or of
+// lanes, where rows are short).  Statistics and sums are FP32.
 //
 // 16384 rows of 4096 columns, BF16: forward 47-52 us (5.2-5.7 TB/s), gradient 79 us
 // (73 us and 5.6 TB/s for the rows, 5 us for the weight gradient's last sums).
 // A sum of 8192 such rows, FP32 stream and BF16 branch: 78 us (5.2 TB/s); its
-// gradient of 5003 x 5120 82 us (5.0).  Non-temporal accesses are level.
+// gradient of 5003 x 5120 82 us (5.0).  Non-temporal accesses are level.  The
+// gradient's kernels with two groups to a lane (rows of more than 8192 columns)
+// spill 20 to 84 registers: 3.0 to 3.8 TB/s.
 #pragma once
 #include "dropout_kernels.h"
 

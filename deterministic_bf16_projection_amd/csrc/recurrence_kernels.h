@@ -34,7 +34,7 @@
 // 256 bytes walked by one workgroup each, reaches 5.5 TB/s with two reads and a
 // write and 5.3 with three and two (rows of 128 bytes, two reads and a write:
 // 4.5).  8 sequences of 4096 rows, 4096 channels, BF16: forward 155 us (5.2
-// TB/s), gradient 251 us (5.3).  One sequence of 65536 rows, 2048 channels: 238 us
+// TB/s), gradient 254 us (5.3).  One sequence of 65536 rows, 2048 channels: 239 us
 // for its two launches (5.6 TB/s of their five passes).  What it came from:
 // forward 204 us and gradient 477 without a store a tile late and scalar row
 // addresses, 180 and 307 with them; 159 with runs of 256-byte rows; gradient 313

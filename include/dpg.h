@@ -545,8 +545,8 @@ dpg_status dpg_add_layer_norm_dgrad(const void* dy, int64_t lddy, dpg_dtype dy_d
  *              not wanted
  * A weight that is exactly 0 leaves its term out whatever the term is, so a
  * gate of -infinity (any below about -87 counts as one) forgets the state, and
- * one of +infinity with `coupled` passes over the input.  A gate that is NaN
- * makes h NaN from its row on, until a weight of 0.
+ * one of +infinity (any above about 87) with `coupled` passes over the input.  A
+ * gate that is NaN makes h NaN from its row on, until a weight of 0.
  *
  * Gradient, from dh [R, D] of h and dstate [S, D] (or NULL: zeros) of state_out,
  * with the forward call's inputs and what it wrote to `carries`:
